@@ -3,8 +3,11 @@
 The work is done by hand-written HIP kernels in ``libspecverify.so`` behind the
 C ABI of ``include/spec_verify.h`` (verification), ``include/spec_bandit.h``
 (online draft selection), ``include/spec_head.h`` (low-rank draft head with
-its fused normaliser) and ``include/spec_tree.h`` (draft-tree pruning and
-greedy tree verification); this package is a thin ctypes binding with
+its fused normaliser), ``include/spec_tree.h`` (draft-tree pruning and
+greedy tree verification), ``include/spec_beam.h`` (beam selection and the
+reordering of the beams' states), ``include/spec_distill.h`` (distillation from
+a teacher's top logits) and ``include/spec_int8.h`` (row quantisation and the
+8-bit integer product); this package is a thin ctypes binding with
 the same function names (``binding``) and the build script (``build``).
 """
 from .binding import (  # noqa: F401
@@ -23,4 +26,8 @@ from .binding import (  # noqa: F401
     spec_tree_verify_greedy, spec_tree_verify_init, spec_tree_verify_sample,
     spec_tree_verify_set_stream, spec_tree_verify_gave_up, spec_tree_verify_set_spin_limit,
     SPEC_ESCRATCH, SPEC_VERIFY_NOALLOC_SCRATCH_BYTES, spec_verify_noalloc, spec_hbm_read_probe,
+    SPEC_BEAM_MAX, BeamContext, spec_beam_destroy, spec_beam_init, spec_beam_reorder,
+    spec_beam_select, spec_beam_set_stream,
+    SPEC_DISTILL_MAX_K, spec_distill_backward, spec_distill_forward, spec_distill_loss_grad,
+    SPEC_INT8_MAX_DEPTH, spec_int8_product, spec_quantize_rows,
 )

@@ -42,7 +42,15 @@ EXPORTED = (
     "spec_tree_verify_greedy", "spec_tree_verify_sample", "spec_tree_verify_destroy",
     "spec_tree_verify_gave_up", "spec_tree_verify_set_spin_limit",
     "spec_verify_noalloc", "spec_hbm_read_probe",
+    "spec_beam_init", "spec_beam_set_stream", "spec_beam_select", "spec_beam_destroy",
+    "spec_beam_reorder",
+    "spec_distill_forward", "spec_distill_backward", "spec_distill_loss_grad",
+    "spec_quantize_rows", "spec_int8_product",
 )
+
+SPEC_BEAM_MAX = 64
+SPEC_DISTILL_MAX_K = 256
+SPEC_INT8_MAX_DEPTH = 131056
 
 SPEC_TREE_MAX_NODES = 256
 
@@ -71,6 +79,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(f"{path} is not built; run __graft_entry__.build() first")
     lib = ctypes.CDLL(path)
     P, i32, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64
+    i64 = ctypes.c_int64
     sig = {
         "spec_verify_init": ([i32, i32, i32, i32, P, ctypes.POINTER(P)], i32),
         "spec_verify_set_stream": ([P, P], i32),
@@ -107,6 +116,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_tree_verify_destroy": ([P], i32),
         "spec_tree_verify_gave_up": ([P, ctypes.POINTER(u64)], i32),
         "spec_tree_verify_set_spin_limit": ([P, i32], i32),
+        "spec_beam_init": ([i32, i32, i32, i32, i32, P, ctypes.POINTER(P)], i32),
+        "spec_beam_set_stream": ([P, P], i32),
+        "spec_beam_select": ([P, P, P, P, P, P, P, P], i32),
+        "spec_beam_destroy": ([P], i32),
+        "spec_beam_reorder": ([i32, i32, i32, i32, P, P, i64, P, i64, i64, P], i32),
+        "spec_distill_forward": ([i32, i32, i32, i32, P, P, P, P, P, P, P, P], i32),
+        "spec_distill_backward": ([i32, i32, i32, i32, P, P, P, P, P, P, P, P, P], i32),
+        "spec_distill_loss_grad": ([i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P], i32),
+        "spec_quantize_rows": ([i32, i32, i32, P, P, P, P], i32),
+        "spec_int8_product": ([i32, i32, i32, P, P, P, P, i32, P, P], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -589,3 +608,189 @@ def spec_tree_verify_destroy(ctx: TreeContext) -> None:
         rc = load_library().spec_tree_verify_destroy(ctx.handle)
         ctx.handle = None
         _check("spec_tree_verify_destroy", rc)
+
+
+def _on_current_device(*tensors) -> None:
+    """The draft operators launch on the current device: a tensor on another one is refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+class BeamContext:
+    """Owns a spec_beam_ctx*; destroyed with spec_beam_destroy."""
+
+    def __init__(self, handle: ctypes.c_void_p, batch: int, beams: int, keep: int, vocab: int,
+                 dtype: int, device: int):
+        self.handle = handle
+        self.batch, self.beams, self.keep, self.vocab = batch, beams, keep, vocab
+        self.dtype, self.device = dtype, device
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            try:
+                load_library().spec_beam_destroy(self.handle)
+            except Exception:
+                pass
+            self.handle = None
+
+
+def spec_beam_init(batch: int, beams: int, keep: int, vocab: int, dtype, stream=None) -> BeamContext:
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    h = ctypes.c_void_p()
+    _check("spec_beam_init", load_library().spec_beam_init(
+        batch, beams, keep, vocab, code, _stream_handle(stream), ctypes.byref(h)))
+    return BeamContext(h, batch, beams, keep, vocab, code, torch.cuda.current_device())
+
+
+def spec_beam_set_stream(ctx: BeamContext, stream=None) -> None:
+    _check("spec_beam_set_stream",
+           load_library().spec_beam_set_stream(ctx.handle, _stream_handle(stream)))
+
+
+def spec_beam_select(ctx: BeamContext, logits, score, lse, out_parent, out_token, out_score,
+                     out_logq=None) -> None:
+    """The `keep` best continuations over beams and vocabulary: logits [B, W, V] in the
+    context's dtype, score [B, W] float32 (-inf: no beam), lse [B, W] float64 row
+    normalisers or None (formed by the call); out_parent, out_token [B, K] int32,
+    out_score, out_logq [B, K] float32 (out_logq may be None)."""
+    B, W, K, V = ctx.batch, ctx.beams, ctx.keep, ctx.vocab
+    ldt = torch.bfloat16 if ctx.dtype == SPEC_BF16 else torch.float32
+    _expect(logits, (B, W, V), ldt, "logits")
+    _expect(score, (B, W), torch.float32, "score")
+    _expect(lse, (B, W), torch.float64, "lse")
+    _expect(out_parent, (B, K), torch.int32, "out_parent")
+    _expect(out_token, (B, K), torch.int32, "out_token")
+    _expect(out_score, (B, K), torch.float32, "out_score")
+    _expect(out_logq, (B, K), torch.float32, "out_logq")
+    _on_current_device(logits, score, lse, out_parent, out_token, out_score, out_logq)
+    if ctx.device != logits.device.index:
+        raise ValueError(f"the context lives on cuda:{ctx.device}, the tensors on {logits.device}")
+    _check("spec_beam_select", load_library().spec_beam_select(
+        ctx.handle, _ptr(logits), _ptr(score), _ptr(lse), _ptr(out_parent), _ptr(out_token),
+        _ptr(out_score), _ptr(out_logq)))
+
+
+def spec_beam_destroy(ctx: BeamContext) -> None:
+    if ctx.handle:
+        rc = load_library().spec_beam_destroy(ctx.handle)
+        ctx.handle = None
+        _check("spec_beam_destroy", rc)
+
+
+def spec_beam_reorder(parent, src, dst, used_bytes: int | None = None, stream=None) -> None:
+    """dst[l, b, j] = src[l, b, parent[b, j]] for parents inside src's beams, other slots left
+    as they are: parent [B, K] int32, src [L, B, W, ...] and dst [L, B, K, ...] of one dtype
+    and state shape; dst may be src (reordered in place). used_bytes moves a prefix of each
+    state only."""
+    if src.dim() < 3 or dst.dim() != src.dim():
+        raise ValueError("src and dst are [layers, batch, beams, ...]")
+    L, B, W = src.shape[:3]
+    K = dst.shape[2]
+    _expect(src, src.shape, src.dtype, "src")
+    _expect(dst, (L, B, K, *src.shape[3:]), src.dtype, "dst")
+    _expect(parent, (B, K), torch.int32, "parent")
+    _on_current_device(parent, src, dst)
+    state = src.element_size()
+    for n in src.shape[3:]:
+        state *= n
+    used = state if used_bytes is None else int(used_bytes)
+    if not 0 <= used <= state:
+        raise ValueError(f"used_bytes: {used}, a state has {state}")
+    _check("spec_beam_reorder", load_library().spec_beam_reorder(
+        L, B, W, K, _ptr(parent), _ptr(src), state, _ptr(dst), state, used,
+        _stream_handle(stream)))
+
+
+def _distill_inputs(logits, ids, teacher, teacher_lse, temperature):
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits are [N, V], ids [N, K]")
+    N, V = logits.shape
+    K = ids.shape[1]
+    code = dtype_code(logits.dtype)
+    _expect(logits, (N, V), logits.dtype, "logits")
+    _expect(ids, (N, K), torch.int32, "ids")
+    _expect(teacher, (N, K), torch.float32, "teacher")
+    _expect(teacher_lse, (N,), torch.float64, "teacher_lse")
+    _expect(temperature, (N,), torch.float32, "temperature")
+    return N, V, K, code
+
+
+def spec_distill_forward(logits, ids, teacher, teacher_lse, temperature, out_loss, out_lse,
+                         stream=None) -> None:
+    """Divergence of each row of logits [N, V] from its teacher's top entries: ids [N, K]
+    int32 (negative: unused), teacher [N, K] float32 logits, teacher_lse [N] float64 or None
+    (normalised over the list), temperature [N] float32; out_loss [N] float32, out_lse [N]
+    float64 (what the backward call takes)."""
+    N, V, K, code = _distill_inputs(logits, ids, teacher, teacher_lse, temperature)
+    _expect(out_loss, (N,), torch.float32, "out_loss")
+    _expect(out_lse, (N,), torch.float64, "out_lse")
+    _on_current_device(logits, ids, teacher, teacher_lse, temperature, out_loss, out_lse)
+    _check("spec_distill_forward", load_library().spec_distill_forward(
+        N, V, code, K, _ptr(logits), _ptr(ids), _ptr(teacher), _ptr(teacher_lse),
+        _ptr(temperature), _ptr(out_loss), _ptr(out_lse), _stream_handle(stream)))
+
+
+def spec_distill_backward(logits, ids, teacher, teacher_lse, temperature, lse, weight, out_grad,
+                          stream=None) -> None:
+    """Gradient of sum_n weight[n] * loss[n] for the logits: lse [N] float64 from the forward
+    call, weight [N] float32; out_grad [N, V] in the logits' dtype (may be the logits)."""
+    N, V, K, code = _distill_inputs(logits, ids, teacher, teacher_lse, temperature)
+    _expect(lse, (N,), torch.float64, "lse")
+    _expect(weight, (N,), torch.float32, "weight")
+    _expect(out_grad, (N, V), logits.dtype, "out_grad")
+    _on_current_device(logits, ids, teacher, teacher_lse, temperature, lse, weight, out_grad)
+    _check("spec_distill_backward", load_library().spec_distill_backward(
+        N, V, code, K, _ptr(logits), _ptr(ids), _ptr(teacher), _ptr(teacher_lse),
+        _ptr(temperature), _ptr(lse), _ptr(weight), _ptr(out_grad), _stream_handle(stream)))
+
+
+def spec_distill_loss_grad(logits, ids, teacher, teacher_lse, temperature, weight, out_loss,
+                           out_lse, out_grad, stream=None) -> None:
+    """spec_distill_forward and spec_distill_backward in one call."""
+    N, V, K, code = _distill_inputs(logits, ids, teacher, teacher_lse, temperature)
+    _expect(weight, (N,), torch.float32, "weight")
+    _expect(out_loss, (N,), torch.float32, "out_loss")
+    _expect(out_lse, (N,), torch.float64, "out_lse")
+    _expect(out_grad, (N, V), logits.dtype, "out_grad")
+    _on_current_device(logits, ids, teacher, teacher_lse, temperature, weight, out_loss, out_lse,
+                       out_grad)
+    _check("spec_distill_loss_grad", load_library().spec_distill_loss_grad(
+        N, V, code, K, _ptr(logits), _ptr(ids), _ptr(teacher), _ptr(teacher_lse),
+        _ptr(temperature), _ptr(weight), _ptr(out_loss), _ptr(out_lse), _ptr(out_grad),
+        _stream_handle(stream)))
+
+
+def spec_quantize_rows(x, out_q, out_scale, stream=None) -> None:
+    """x [N, D] float32 or bfloat16 to 8 bits with a scale for each row: out_q [N, D] int8,
+    out_scale [N] float32."""
+    if x.dim() != 2:
+        raise ValueError("x is [N, D]")
+    N, D = x.shape
+    code = dtype_code(x.dtype)
+    _expect(x, (N, D), x.dtype, "x")
+    _expect(out_q, (N, D), torch.int8, "out_q")
+    _expect(out_scale, (N,), torch.float32, "out_scale")
+    _on_current_device(x, out_q, out_scale)
+    _check("spec_quantize_rows", load_library().spec_quantize_rows(
+        N, D, code, _ptr(x), _ptr(out_q), _ptr(out_scale), _stream_handle(stream)))
+
+
+def spec_int8_product(a, a_scale, w, w_scale, out, stream=None) -> None:
+    """out[n, v] = sum_k a[n, k] w[v, k] * a_scale[n] * w_scale[v]: a [N, D] and w [V, D] int8,
+    scales float32, out [N, V] float32 or bfloat16."""
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a is [N, D], w is [V, D]")
+    N, D = a.shape
+    V = w.shape[0]
+    code = dtype_code(out.dtype)
+    _expect(a, (N, D), torch.int8, "a")
+    _expect(a_scale, (N,), torch.float32, "a_scale")
+    _expect(w, (V, D), torch.int8, "w")
+    _expect(w_scale, (V,), torch.float32, "w_scale")
+    _expect(out, (N, V), out.dtype, "out")
+    _on_current_device(a, a_scale, w, w_scale, out)
+    _check("spec_int8_product", load_library().spec_int8_product(
+        N, D, V, _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), code, _ptr(out),
+        _stream_handle(stream)))

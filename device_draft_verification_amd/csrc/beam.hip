@@ -1,0 +1,634 @@
+// Beam selection over beams and vocabulary, and the reordering of the beams'
+// states (spec_beam.h).
+//
+//   value(w, v) = score[w] + (z[w][v] - lse[w]), the K best of W * V.
+//
+// Within a beam the value never falls with the logit, so a beam's part of the
+// answer is among the K first of its row in the order (larger z, lower v), and
+// that order is the order of one 64-bit integer, (ordered bits of z) << 32 |
+// ~v. Two kernels:
+//   beam_piece: one workgroup per piece of a row; the piece stays in registers
+//     while its K largest keys are found, so the logits are read once;
+//   beam_merge: one workgroup per sequence; forms the binary64 values of the
+//     pieces' keys and keeps the K best over the beams.
+// Both narrow by the K-th largest of their threads' largest entries (at least K
+// entries reach it, and few more do), collect what reaches it in LDS, and rank
+// the collected entries by counting. Collected in any order, ranked by a total
+// order: the result does not depend on timing.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <new>
+
+#include "rows.hpp"
+#include "spec_beam.h"
+
+namespace specv {
+namespace {
+
+constexpr int kPieceUnroll = 8;          // 16-byte groups of a piece per thread
+constexpr int kCollect = kBlock;         // collected entries: one per thread when ranked
+// log2(e) minus its binary32 rounding: the exponent's second term keeps the
+// normaliser's error at the rounding of single exponentials instead of 1.3e-8
+// times the distance from the row's maximum.
+constexpr float kLog2eLow = 1.92596299e-8f;
+
+struct NormPart {
+    float m;  // the piece's largest finite logit (-inf: none)
+    int pad;
+    double s;  // sum of exp(z - m)  (m = 0 when there is none)
+};
+
+__device__ inline uint32_t ordered32(float z) {
+    const uint32_t b = __float_as_uint(z);
+    return b ^ (b & 0x80000000u ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ inline float unordered32(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ inline uint64_t ordered64(double x) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x));
+    return b ^ (b >> 63 ? ~0ull : 1ull << 63);
+}
+__device__ inline double unordered64(uint64_t o) {
+    return __longlong_as_double(static_cast<long long>(o >> 63 ? o ^ (1ull << 63) : ~o));
+}
+
+// Key of a candidate; 0 marks no candidate (a finite z never has it).
+__device__ inline uint64_t make_key(float z, int v) {
+    return static_cast<uint64_t>(ordered32(z)) << 32 | ~static_cast<uint32_t>(v);
+}
+__device__ inline float key_logit(uint64_t k) { return unordered32(static_cast<uint32_t>(k >> 32)); }
+__device__ inline int key_token(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
+
+// The wavefront's values sorted, largest first (bitonic).
+template <typename T>
+__device__ inline T wave_sort(T v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 2; k <= 64; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            const T o = __shfl_xor(v, j, 64);
+            const bool keep_max = ((lane & j) == 0) == ((lane & k) == 0);
+            v = (o > v) == keep_max ? o : v;
+        }
+    return v;
+}
+
+// The keep-th largest of the workgroup's values, one per thread (keep <= 64).
+// Every wavefront sorts its own; a thread's place in the whole is its place in
+// its own list plus the entries before it in the others. sorted: kWaves * 64
+// values of LDS, result: one. Equal values are placed by wavefront.
+template <typename T>
+__device__ inline T kth_largest(T v, int keep, T* sorted, T* result) {
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    v = wave_sort(v);
+    sorted[wid * 64 + lane] = v;
+    __syncthreads();
+    int place = lane;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wid)
+            continue;
+        const T* list = sorted + w * 64;
+        int lo = 0;  // entries of the list before v
+#pragma unroll
+        for (int step = 64; step > 0; step >>= 1) {
+            const int at = lo + step - 1;
+            if (at < 64 && (w < wid ? list[at] >= v : list[at] > v))
+                lo += step;
+        }
+        place += lo;
+    }
+    if (place == keep - 1)
+        *result = v;
+    __syncthreads();
+    return *result;
+}
+
+__device__ inline uint64_t block_max_u64(uint64_t v, uint64_t* lds) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const uint64_t o = __shfl_xor(static_cast<unsigned long long>(v), off, 64);
+        v = o > v ? o : v;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+        v = lds[w] > v ? lds[w] : v;
+    return v;
+}
+
+// The K largest keys of piece p of row `row`, largest first, 0 where the piece
+// has fewer candidates; with NORM also the piece's part of the normaliser.
+template <int DT, int U, bool NORM>
+__global__ __launch_bounds__(kBlock) void beam_piece_kernel(
+    const void* __restrict__ logits, const float* __restrict__ score,
+    const double* __restrict__ lse, int vocab, int keep, int pieces, uint64_t* __restrict__ keys,
+    NormPart* __restrict__ norm) {
+    using Row = RowGroups<DT>;
+    constexpr int W = Row::W;
+    const long row = blockIdx.x / static_cast<unsigned>(pieces);
+    const int p = static_cast<int>(blockIdx.x % static_cast<unsigned>(pieces));
+    uint64_t* out = keys + (row * pieces + p) * keep;
+    const int tid = threadIdx.x;
+
+    const float sc = score[row];
+    if (!is_finite_f32(sc) || (!NORM && !is_finite_f64(lse[row]))) {
+        if (tid < keep)
+            out[tid] = 0;
+        return;
+    }
+    const Row r(row_ptr(logits, DT, row, vocab), vocab);
+    const int g0 = static_cast<int>(static_cast<long>(r.groups) * p / pieces);
+    const int g1 = static_cast<int>(static_cast<long>(r.groups) * (p + 1) / pieces);
+    uint4 q[U];
+    r.template load<U, kBlock>(g0 + tid, g1, q);
+
+    __shared__ float sorted[kBlock];
+    __shared__ float kth;
+    __shared__ uint64_t list[kCollect];
+    __shared__ uint64_t lds64[kWaves];
+    __shared__ int count;
+    if (tid == 0)
+        count = 0;
+
+    const float inf = __builtin_huge_valf();
+    float best = -inf;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float z[W];
+        Row::unpack(q[u], z);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            best = fmaxf(best, z[e]);
+    }
+    if (best == inf) {  // an infinite logit is no candidate
+        best = -inf;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[W];
+            Row::unpack(q[u], z);
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                best = z[e] < inf ? fmaxf(best, z[e]) : best;
+        }
+    }
+    const float bar = kth_largest(best, keep, sorted, &kth);
+
+    if constexpr (NORM) {
+        float m = sorted[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w)
+            m = fmaxf(m, sorted[w * 64]);
+        const float ref = m == -inf ? 0.0f : m;
+        double s = 0.0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[W];
+            Row::unpack(q[u], z);
+            float g = 0.0f;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float t = z[e] - ref;
+                g += fast_exp2(__builtin_fmaf(t, kLog2e, t * kLog2eLow));
+            }
+            s += static_cast<double>(g);
+        }
+        s = block_sum(s, reinterpret_cast<double*>(lds64));
+        if (tid == 0)
+            norm[row * pieces + p] = NormPart{m, 0, s};
+    }
+
+    if (best >= bar && best > -inf) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[W];
+            Row::unpack(q[u], z);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (z[e] >= bar && is_finite_f32(z[e])) {
+                    const int slot = atomicAdd(&count, 1);
+                    if (slot < kCollect)
+                        list[slot] = make_key(z[e], static_cast<int>(r.element(g0 + tid + u * kBlock) + e));
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int n = count;
+    if (n <= kCollect) {
+        if (tid < n) {
+            const uint64_t mine = list[tid];
+            int place = 0;
+            for (int i = 0; i < n; ++i)
+                place += list[i] > mine;
+            if (place < keep)
+                out[place] = mine;
+        } else if (tid < keep) {
+            out[tid] = 0;
+        }
+        return;
+    }
+    // More entries tie at the bar than the list holds: take the largest
+    // remaining key keep times. n > kCollect >= keep, so all keep exist.
+    uint64_t last = ~0ull;
+    for (int k = 0; k < keep; ++k) {
+        uint64_t mine = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[W];
+            Row::unpack(q[u], z);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (z[e] >= bar && is_finite_f32(z[e])) {
+                    const uint64_t key = make_key(z[e], static_cast<int>(r.element(g0 + tid + u * kBlock) + e));
+                    mine = key < last && key > mine ? key : mine;
+                }
+            }
+        }
+        last = block_max_u64(mine, lds64);
+        if (tid == 0)
+            out[k] = last;
+    }
+}
+
+// A candidate of the merge in its total order: value, then the lower beam, then
+// the larger key (larger logit, lower token). value 0: none.
+struct Cand {
+    uint64_t value;
+    uint64_t key;
+    int beam;
+};
+
+__device__ inline bool before(const Cand& a, const Cand& b) {
+    if (a.value != b.value)
+        return a.value > b.value;
+    if (a.beam != b.beam)
+        return a.beam < b.beam;
+    return a.key > b.key;
+}
+
+template <bool NORM>
+__global__ __launch_bounds__(kBlock) void beam_merge_kernel(
+    const float* __restrict__ score, const double* __restrict__ lse, int beams, int keep,
+    int pieces, const uint64_t* __restrict__ keys, const NormPart* __restrict__ norm,
+    int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
+    __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
+    __shared__ int alive[SPEC_BEAM_MAX];
+    __shared__ uint64_t sorted[kBlock];
+    __shared__ uint64_t kth;
+    __shared__ Cand list[kCollect];
+    __shared__ Cand wave_best[kWaves];
+    __shared__ int count;
+    const long b = blockIdx.x;
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        count = 0;
+    for (int w = tid; w < beams; w += kBlock) {
+        const long row = b * beams + w;
+        const float sc = score[row];
+        bool ok = is_finite_f32(sc);
+        double l = 0.0;
+        if constexpr (NORM) {
+            if (ok) {
+                // log sum over the pieces, against the largest piece maximum
+                const NormPart* part = norm + row * pieces;
+                float m = -__builtin_huge_valf();
+                for (int p = 0; p < pieces; ++p)
+                    m = fmaxf(m, part[p].m);
+                double s = 0.0;
+                for (int p = 0; p < pieces; ++p) {
+                    const NormPart x = part[p];
+                    // a piece without a finite logit has sum 0, or NaN or inf
+                    s += x.m == -__builtin_huge_valf()
+                             ? x.s
+                             : x.s * exp(static_cast<double>(x.m) - static_cast<double>(m));
+                }
+                l = static_cast<double>(m) + log(s);
+            }
+        } else {
+            l = lse[row];
+        }
+        ok = ok && is_finite_f64(l);
+        b_score[w] = static_cast<double>(sc);
+        b_lse[w] = l;
+        alive[w] = ok;
+    }
+    __syncthreads();
+
+    const int per_beam = pieces * keep, total = beams * per_beam;
+    const uint64_t* k_b = keys + b * total;
+    auto candidate = [&](int c) {
+        const int w = c / per_beam;
+        const uint64_t key = k_b[c];
+        Cand x{0, key, w};
+        if (key != 0 && alive[w])
+            x.value = ordered64(b_score[w] + (static_cast<double>(key_logit(key)) - b_lse[w]));
+        return x;
+    };
+    uint64_t best = 0;
+    for (int c = tid; c < total; c += kBlock) {
+        const uint64_t v = candidate(c).value;
+        best = v > best ? v : best;
+    }
+    const uint64_t bar = kth_largest(best, keep, sorted, &kth);
+    if (best >= bar && best != 0) {
+        for (int c = tid; c < total; c += kBlock) {
+            const Cand x = candidate(c);
+            if (x.value >= bar && x.value != 0) {
+                const int slot = atomicAdd(&count, 1);
+                if (slot < kCollect)
+                    list[slot] = x;
+            }
+        }
+    }
+    __syncthreads();
+    const int n = count;
+    auto emit = [&](int j, const Cand& x) {
+        const long at = b * keep + j;
+        const bool some = x.value != 0;
+        out_parent[at] = some ? x.beam : -1;
+        out_token[at] = some ? key_token(x.key) : -1;
+        out_score[at] = some ? static_cast<float>(unordered64(x.value)) : -__builtin_huge_valf();
+        if (out_logq)
+            out_logq[at] = some ? static_cast<float>(static_cast<double>(key_logit(x.key)) - b_lse[x.beam])
+                                : -__builtin_huge_valf();
+    };
+    if (n <= kCollect) {
+        if (tid < n) {
+            const Cand mine = list[tid];
+            int place = 0;
+            for (int i = 0; i < n; ++i)
+                place += before(list[i], mine);
+            if (place < keep)
+                emit(place, mine);
+        } else if (tid < keep) {
+            emit(tid, Cand{0, 0, 0});
+        }
+        return;
+    }
+    // More ties than the list holds: the best remaining candidate, keep times.
+    Cand last{~0ull, ~0ull, -1};
+    for (int k = 0; k < keep; ++k) {
+        Cand mine{0, 0, 0};
+        for (int c = tid; c < total; c += kBlock) {
+            const Cand x = candidate(c);
+            if (x.value != 0 && before(last, x) && (mine.value == 0 || before(x, mine)))
+                mine = x;
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            Cand o;
+            o.value = __shfl_xor(static_cast<unsigned long long>(mine.value), off, 64);
+            o.key = __shfl_xor(static_cast<unsigned long long>(mine.key), off, 64);
+            o.beam = __shfl_xor(mine.beam, off, 64);
+            if (o.value != 0 && (mine.value == 0 || before(o, mine)))
+                mine = o;
+        }
+        __syncthreads();
+        if ((tid & 63) == 0)
+            wave_best[tid >> 6] = mine;
+        __syncthreads();
+        last = wave_best[0];
+        for (int w = 1; w < kWaves; ++w)
+            if (wave_best[w].value != 0 && (last.value == 0 || before(wave_best[w], last)))
+                last = wave_best[w];
+        if (tid == 0)
+            emit(k, last);
+    }
+}
+
+// ---------------------------------------------------------------- reorder ---
+
+// One thread owns one T-sized column of every slot of a (layer, sequence): it
+// reads the parents' columns before it writes any slot, so an in-place
+// permutation needs no other order.
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T, int NB>
+__global__ __launch_bounds__(kBlock) void beam_reorder_kernel(
+    long states, int batch, int beams_in, int beams_out, const int32_t* __restrict__ parent,
+    const char* src, long src_stride, char* dst, long dst_stride, long cols, bool in_place) {
+    const long blocks_per = (cols + kBlock - 1) / kBlock;
+    for (long blk = blockIdx.x; blk < states * blocks_per; blk += gridDim.x) {
+        const long lb = blk / blocks_per;
+        const long col = (blk % blocks_per) * kBlock + threadIdx.x;
+        if (col >= cols)
+            continue;
+        const int32_t* par = parent + (lb % batch) * beams_out;
+        const char* s = src + lb * beams_in * src_stride + col * static_cast<long>(sizeof(T));
+        char* d = dst + lb * beams_out * dst_stride + col * static_cast<long>(sizeof(T));
+        for (int j0 = 0; j0 < beams_out; j0 += NB) {
+            T r[NB] = {};
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int w = j0 + j < beams_out ? par[j0 + j] : -1;
+                if (w >= 0 && w < beams_in && !(in_place && w == j0 + j))
+                    r[j] = *reinterpret_cast<const T*>(s + w * src_stride);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int w = j0 + j < beams_out ? par[j0 + j] : -1;
+                if (w >= 0 && w < beams_in && !(in_place && w == j0 + j))
+                    *reinterpret_cast<T*>(d + (j0 + j) * dst_stride) = r[j];
+            }
+        }
+    }
+}
+
+template <typename T>
+hipError_t launch_reorder(long states, int batch, int beams_in, int beams_out,
+                          const int32_t* parent, const void* src, long src_stride, void* dst,
+                          long dst_stride, long bytes, bool in_place, hipStream_t stream) {
+    const long cols = bytes / static_cast<long>(sizeof(T));
+    const long blocks = states * ((cols + kBlock - 1) / kBlock);
+    const dim3 grid(static_cast<unsigned>(blocks < (1L << 20) ? blocks : 1L << 20));
+    const char* s = static_cast<const char*>(src);
+    char* d = static_cast<char*>(dst);
+    // In place all slots of a column are in registers at once.
+#define SPEC_REORDER(NB)                                                                        \
+    beam_reorder_kernel<T, NB><<<grid, dim3(kBlock), 0, stream>>>(                              \
+        states, batch, beams_in, beams_out, parent, s, src_stride, d, dst_stride, cols, in_place)
+    if (beams_out <= 4)
+        SPEC_REORDER(4);
+    else if (beams_out <= 8 || !in_place)
+        SPEC_REORDER(8);
+    else if (beams_out <= 16)
+        SPEC_REORDER(16);
+    else if (beams_out <= 32)
+        SPEC_REORDER(32);
+    else
+        SPEC_REORDER(64);
+#undef SPEC_REORDER
+    return hipGetLastError();
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace specv
+
+using namespace specv;
+
+struct spec_beam_ctx {
+    int B = 0, W = 0, K = 0, V = 0, dtype = 0, pieces = 0;
+    hipStream_t stream = nullptr;
+    void* ws = nullptr;
+    uint64_t* keys = nullptr;
+    NormPart* norm = nullptr;
+};
+
+extern "C" {
+
+int spec_beam_init(int batch, int beams, int keep, int vocab, int dtype, void* hip_stream,
+                   spec_beam_ctx** out_ctx) {
+    if (!out_ctx)
+        return SPEC_EINVAL;
+    *out_ctx = nullptr;
+    if (batch < 1 || beams < 1 || beams > SPEC_BEAM_MAX || keep < 1 || keep > SPEC_BEAM_MAX ||
+        vocab < 1 || (dtype != SPEC_F32 && dtype != SPEC_BF16))
+        return SPEC_EINVAL;
+    // A row holds at most one group more than its elements need (its first
+    // and last groups may both hang over).
+    const long W = dtype == SPEC_BF16 ? 8 : 4;
+    const long groups = (static_cast<long>(vocab) + W - 1) / W + 1;
+    const long pieces = (groups + kPieceUnroll * kBlock - 1) / (kPieceUnroll * kBlock);
+    const long rows = static_cast<long>(batch) * beams;
+    if (rows * pieces >= (1L << 32) / kBlock || static_cast<long>(beams) * pieces * keep >= (1L << 31))
+        return SPEC_EINVAL;
+    spec_beam_ctx* ctx = new (std::nothrow) spec_beam_ctx();
+    if (!ctx)
+        return SPEC_ENOMEM;
+    ctx->B = batch;
+    ctx->W = beams;
+    ctx->K = keep;
+    ctx->V = vocab;
+    ctx->dtype = dtype;
+    ctx->pieces = static_cast<int>(pieces);
+    ctx->stream = static_cast<hipStream_t>(hip_stream);
+    const size_t key_bytes = static_cast<size_t>(rows) * pieces * keep * sizeof(uint64_t);
+    const size_t norm_bytes = static_cast<size_t>(rows) * pieces * sizeof(NormPart);
+    if (hipMalloc(&ctx->ws, key_bytes + norm_bytes) != hipSuccess) {
+        (void)hipGetLastError();
+        delete ctx;
+        return SPEC_ENOMEM;
+    }
+    // 16-byte entries first: the keys behind them stay aligned
+    ctx->norm = static_cast<NormPart*>(ctx->ws);
+    ctx->keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ctx->ws) + norm_bytes);
+    *out_ctx = ctx;
+    return SPEC_OK;
+}
+
+int spec_beam_set_stream(spec_beam_ctx* ctx, void* hip_stream) {
+    if (!ctx)
+        return SPEC_EINVAL;
+    ctx->stream = static_cast<hipStream_t>(hip_stream);
+    return SPEC_OK;
+}
+
+int spec_beam_select(spec_beam_ctx* ctx, const void* logits, const float* score,
+                     const double* lse, int32_t* out_parent, int32_t* out_token,
+                     float* out_score, float* out_logq) {
+    if (!ctx || !logits || !score || !out_parent || !out_token || !out_score)
+        return SPEC_EINVAL;
+    const size_t esz = ctx->dtype == SPEC_BF16 ? 2 : 4;
+    if (!aligned(logits, esz) || !aligned(score, 4) || (lse && !aligned(lse, 8)) ||
+        !aligned(out_parent, 4) || !aligned(out_token, 4) || !aligned(out_score, 4) ||
+        (out_logq && !aligned(out_logq, 4)))
+        return SPEC_EINVAL;
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(ctx->B) * ctx->W * ctx->pieces));
+    hipStream_t s = ctx->stream;
+#define SPEC_PIECE(DT, NORM)                                                                   \
+    beam_piece_kernel<DT, kPieceUnroll, NORM><<<grid, dim3(kBlock), 0, s>>>(                   \
+        logits, score, lse, ctx->V, ctx->K, ctx->pieces, ctx->keys, ctx->norm)
+    if (ctx->dtype == SPEC_BF16) {
+        if (lse)
+            SPEC_PIECE(kBF16, false);
+        else
+            SPEC_PIECE(kBF16, true);
+    } else {
+        if (lse)
+            SPEC_PIECE(kF32, false);
+        else
+            SPEC_PIECE(kF32, true);
+    }
+#undef SPEC_PIECE
+    if (hipGetLastError() != hipSuccess)
+        return SPEC_EHIP;
+    const dim3 seqs(static_cast<unsigned>(ctx->B));
+    if (lse)
+        beam_merge_kernel<false><<<seqs, dim3(kBlock), 0, s>>>(
+            score, lse, ctx->W, ctx->K, ctx->pieces, ctx->keys, ctx->norm, out_parent, out_token,
+            out_score, out_logq);
+    else
+        beam_merge_kernel<true><<<seqs, dim3(kBlock), 0, s>>>(
+            score, lse, ctx->W, ctx->K, ctx->pieces, ctx->keys, ctx->norm, out_parent, out_token,
+            out_score, out_logq);
+    return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
+}
+
+int spec_beam_destroy(spec_beam_ctx* ctx) {
+    if (!ctx)
+        return SPEC_EINVAL;
+    int rc = SPEC_OK;
+    if (hipStreamSynchronize(ctx->stream) != hipSuccess)
+        rc = SPEC_EHIP;
+    if (ctx->ws && hipFree(ctx->ws) != hipSuccess)
+        rc = SPEC_EHIP;
+    delete ctx;
+    return rc;
+}
+
+int spec_beam_reorder(int layers, int batch, int beams_in, int beams_out, const int32_t* parent,
+                      const void* src, int64_t src_stride, void* dst, int64_t dst_stride,
+                      int64_t bytes, void* hip_stream) {
+    if (layers < 0 || batch < 0 || beams_in < 1 || beams_in > SPEC_BEAM_MAX || beams_out < 1 ||
+        beams_out > SPEC_BEAM_MAX || bytes < 0 || src_stride < bytes || dst_stride < bytes)
+        return SPEC_EINVAL;
+    if (layers == 0 || batch == 0 || bytes == 0)
+        return SPEC_OK;
+    if (!parent || !src || !dst || !aligned(parent, 4))
+        return SPEC_EINVAL;
+    const long states = static_cast<long>(layers) * batch;
+    // Every byte offset has to fit 63 bits.
+    if (src_stride > (INT64_MAX / SPEC_BEAM_MAX) / states || dst_stride > (INT64_MAX / SPEC_BEAM_MAX) / states)
+        return SPEC_EINVAL;
+    const uint64_t src_bytes = static_cast<uint64_t>(states * beams_in - 1) * src_stride + bytes;
+    const uint64_t dst_bytes = static_cast<uint64_t>(states * beams_out - 1) * dst_stride + bytes;
+    const bool in_place = src == dst && src_stride == dst_stride && beams_in == beams_out;
+    if (!in_place && overlap(src, src_bytes, dst, dst_bytes))
+        return SPEC_EINVAL;
+    const uint64_t parent_bytes = static_cast<uint64_t>(batch) * beams_out * sizeof(int32_t);
+    if (overlap(parent, parent_bytes, src, src_bytes) || overlap(parent, parent_bytes, dst, dst_bytes))
+        return SPEC_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    auto fits = [&](int a) {
+        return aligned(src, a) && aligned(dst, a) && src_stride % a == 0 && dst_stride % a == 0 &&
+               bytes % a == 0;
+    };
+    hipError_t e;
+    if (fits(16))
+        e = launch_reorder<u32x4>(states, batch, beams_in, beams_out, parent, src, src_stride, dst,
+                                  dst_stride, bytes, in_place, s);
+    else if (fits(4))
+        e = launch_reorder<uint32_t>(states, batch, beams_in, beams_out, parent, src, src_stride,
+                                     dst, dst_stride, bytes, in_place, s);
+    else
+        e = launch_reorder<uint8_t>(states, batch, beams_in, beams_out, parent, src, src_stride,
+                                    dst, dst_stride, bytes, in_place, s);
+    return e == hipSuccess ? SPEC_OK : SPEC_EHIP;
+}
+
+}  // extern "C"

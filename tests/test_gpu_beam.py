@@ -1,0 +1,349 @@
+"""GPU parity of beam selection (spec_beam_select) and state reordering (spec_beam_reorder)
+against oracle/draft_ops.py.
+
+Match rule. With the normalisers given, a candidate's value is two binary64 additions that the
+definition names: parents and tokens are equal, and the outputs are the oracle's values rounded
+to binary32, bit for bit. With the normalisers formed by the call, each is within
+    e = 2^-23 (ln V + 6)
+of the exact one: a term's exponent t = z - max carries two binary32 roundings, 2 |t| 2^-24,
+whose mean over the row's distribution is at most 2 ln V 2^-24 (the mean of -t is at most the
+entropy, at most ln V); the exponential's last place is 2^-23, and a sum of 8 terms in binary32
+adds at most 7 * 2^-24; together below 2^-24 (2 ln V + 9). So the j-th kept candidate's exact
+value is within 2 e of the oracle's j-th, and the scores are within e plus their rounding.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import device_draft_verification_amd as sv
+from oracle import draft_ops as ops
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def make(B, W, V, dtype, seed, sd=2.5, offset=0):
+    """logits (from element `offset` of a larger buffer on), scores with a dead beam or two."""
+    g = torch.Generator().manual_seed(seed)
+    n = B * W * V
+    flat = torch.zeros(n + offset, dtype=DTYPE[dtype], device="cuda")
+    flat[offset:] = (torch.randn(n, generator=g) * sd).to(DTYPE[dtype]).cuda()
+    logits = flat[offset:].view(B, W, V)
+    score = -torch.rand(B, W, generator=g).cumsum(1)
+    if W > 2:
+        score[0, W // 2] = -math.inf
+        score[-1, 0] = math.nan
+    return logits, score.cuda()
+
+
+def select(logits, score, lse, K, dtype, ctx=None):
+    B, W, V = logits.shape
+    own = ctx is None
+    if own:
+        ctx = sv.spec_beam_init(B, W, K, V, DTYPE[dtype])
+    parent = torch.full((B, K), -7, dtype=torch.int32, device="cuda")
+    token = torch.full((B, K), -7, dtype=torch.int32, device="cuda")
+    sc = torch.full((B, K), 7.0, device="cuda")
+    lq = torch.full((B, K), 7.0, device="cuda")
+    sv.spec_beam_select(ctx, logits, score, lse, parent, token, sc, lq)
+    torch.cuda.synchronize()
+    if own:
+        sv.spec_beam_destroy(ctx)
+    return tuple(t.cpu().numpy() for t in (parent, token, sc, lq))
+
+
+def host(logits):
+    return logits.float().cpu().numpy()
+
+
+def check_given(logits, score, lse, K, dtype):
+    got = select(logits, score, lse, K, dtype)
+    p, t, v, q = ops.beam_select(host(logits), score.cpu().numpy(), lse.cpu().numpy(), K)
+    assert np.array_equal(got[0], p)
+    assert np.array_equal(got[1], t)
+    assert np.array_equal(got[2], v.astype(np.float32))
+    assert np.array_equal(got[3], q.astype(np.float32))
+
+
+def check_formed(logits, score, K, dtype):
+    z, s = host(logits), score.cpu().numpy()
+    B, W, V = z.shape
+    got = select(logits, score, None, K, dtype)
+    lse = ops.row_lse(z)
+    p, t, v, q = ops.beam_select(z, s, None, K)
+    e = 2.0 ** -23 * (math.log(V) + 6)
+    none = p < 0
+    assert np.array_equal(got[0] < 0, none) and np.array_equal(got[1] < 0, none)
+    for b in range(B):
+        seen = set()
+        for j in range(K):
+            if none[b, j]:
+                assert got[2][b, j] == -np.inf and got[3][b, j] == -np.inf
+                continue
+            w, tok = int(got[0][b, j]), int(got[1][b, j])
+            assert (w, tok) not in seen
+            seen.add((w, tok))
+            lq = float(z[b, w, tok]) - lse[b, w]
+            val = float(s[b, w]) + lq
+            assert abs(val - v[b, j]) <= 2 * e, (b, j)
+            half = 2.0 ** -24
+            assert abs(got[2][b, j] - val) <= e + half * (abs(val) + e), (b, j)
+            assert abs(got[3][b, j] - lq) <= e + half * (abs(lq) + e), (b, j)
+
+
+SHAPES = [
+    (1, 1, 1, 1), (1, 1, 1, 5), (2, 3, 7, 4), (1, 4, 257, 4), (3, 5, 1000, 64), (2, 64, 300, 64),
+    (1, 64, 4099, 33), (5, 2, 2048 * 8, 8), (2, 3, 2048 * 8 + 1, 7), (2, 8, 32000, 8), (3, 7, 20011, 10),
+    (1, 3, 128256, 32), (40, 16, 517, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,W,V,K", SHAPES)
+def test_selection_with_given_normalisers(B, W, V, K, dtype):
+    print(f"\n[beam B={B} W={W} V={V} K={K} {dtype}]", flush=True)
+    logits, score = make(B, W, V, dtype, seed=B + W + V + K)
+    check_given(logits, score, torch.logsumexp(logits.double(), -1), K, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,W,V,K", SHAPES)
+def test_selection_with_formed_normalisers(B, W, V, K, dtype):
+    logits, score = make(B, W, V, dtype, seed=B * W + V + K)
+    check_formed(logits, score, K, dtype)
+
+
+@pytest.mark.parametrize("offset", [1, 3, 5, 7])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_any_alignment_of_the_rows(dtype, offset):
+    logits, score = make(2, 3, 5003, dtype, seed=offset, offset=offset)
+    check_given(logits, score, torch.logsumexp(logits.double(), -1), 9, dtype)
+    check_formed(logits, score, 9, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 8, 64])
+def test_ties_go_to_the_lower_beam_and_token(K, dtype):
+    """All logits equal, blocks of equal ones, and few distinct values: more ties than a piece's
+    list holds."""
+    B, W, V = 2, 5, 9000
+    logits = torch.zeros(B, W, V, dtype=DTYPE[dtype], device="cuda")
+    lse = torch.zeros(B, W, dtype=torch.float64, device="cuda")
+    score = torch.zeros(B, W, device="cuda")
+    check_given(logits, score, lse, K, dtype)
+    logits[:, :, 4000:] = 1.0
+    check_given(logits, score, lse, K, dtype)
+    g = torch.Generator().manual_seed(K)
+    logits.copy_(torch.randint(-2, 3, (B, W, V), generator=g))
+    score.copy_(torch.randint(-2, 1, (B, W), generator=g).float())
+    check_given(logits, score, lse, K, dtype)
+    # sorted vocabularies: the best entries are neighbours
+    logits.copy_(torch.arange(V, 0, -1).div(64).floor())
+    check_given(logits, score, lse, K, dtype)
+
+
+def test_logits_of_one_beam_that_round_to_one_value():
+    """Logits so close to zero that adding the normaliser loses their difference: within a beam
+    the larger logit comes first, and a beam's candidates stay together before the next one's."""
+    z = torch.full((1, 2, 64), -5.0, device="cuda")
+    z[0, :, 10], z[0, :, 20], z[0, :, 30] = 1e-30, 3e-30, 2e-30
+    lse = torch.full((1, 2), 3.0, dtype=torch.float64, device="cuda")
+    score = torch.zeros(1, 2, device="cuda")
+    check_given(z, score, lse, 5, "f32")
+    got = select(z, score, lse, 5, "f32")
+    assert got[0].tolist() == [[0, 0, 0, 1, 1]] and got[1].tolist() == [[20, 30, 10, 20, 30]]
+
+
+def test_infinities_and_nan_are_no_candidates():
+    for dtype in ("f32", "bf16"):
+        logits, score = make(3, 4, 3001, dtype, seed=1)
+        logits[0, 0, :2990] = -math.inf             # a masked vocabulary
+        logits[0, 1] = -math.inf                    # a beam with nothing left
+        logits[1, 2, 17] = math.inf
+        logits[1, 1, 5] = math.nan
+        logits[1, 3, 2048:2060] = math.nan
+        lse = torch.randn(3, 4, dtype=torch.float64, device="cuda")
+        lse[2, 1], lse[2, 2], lse[2, 3] = math.nan, math.inf, -math.inf
+        score[0, 3] = math.inf
+        check_given(logits, score, lse, 40, dtype)
+        with np.errstate(all="ignore"):
+            check_formed(logits, score, 40, dtype)  # rows 1, 2 and 3 of sequence 1 have no normaliser
+
+
+def test_no_candidate_at_all():
+    logits, score = make(2, 2, 100, "f32", seed=1)
+    score.fill_(-math.inf)
+    p, t, s, q = select(logits, score, None, 3, "f32")
+    assert (p == -1).all() and (t == -1).all() and (s == -np.inf).all() and (q == -np.inf).all()
+
+
+def test_repeated_calls_are_equal_and_scores_may_be_updated_in_place():
+    B, W, V = 4, 8, 30011
+    logits, score = make(B, W, V, "bf16", seed=2)
+    ctx = sv.spec_beam_init(B, W, W, V, torch.bfloat16)
+    first = select(logits, score, None, W, "bf16", ctx)
+    for _ in range(20):
+        again = select(logits, score, None, W, "bf16", ctx)
+        assert all(np.array_equal(x, y, equal_nan=True) for x, y in zip(first, again))
+    parent = torch.empty(B, W, dtype=torch.int32, device="cuda")
+    token = torch.empty_like(parent)
+    sv.spec_beam_select(ctx, logits, score, None, parent, token, score)     # no logq, in place
+    torch.cuda.synchronize()
+    assert np.array_equal(score.cpu().numpy(), first[2])
+    assert np.array_equal(parent.cpu().numpy(), first[0])
+
+
+def test_selection_on_a_side_stream():
+    logits, score = make(2, 4, 20000, "bf16", seed=5)
+    lse = torch.logsumexp(logits.double(), -1)
+    want = select(logits, score, lse, 6, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ctx = sv.spec_beam_init(2, 4, 6, 20000, torch.bfloat16)
+        got = select(logits, score, lse, 6, "bf16", ctx)
+    assert all(np.array_equal(x, y) for x, y in zip(want, got))
+    sv.spec_beam_set_stream(ctx, torch.cuda.current_stream())
+    got = select(logits, score, lse, 6, "bf16", ctx)
+    assert all(np.array_equal(x, y) for x, y in zip(want, got))
+
+
+def test_step_replayed_from_a_graph():
+    """Selection and in-place reordering captured once; replays on new inputs equal eager calls."""
+    L, B, W, V, S = 2, 3, 6, 12007, 80
+    ctx = sv.spec_beam_init(B, W, W, V, torch.bfloat16)
+    logits, score = make(B, W, V, "bf16", seed=9)
+    state = torch.randn(L, B, W, S, device="cuda")
+    parent = torch.empty(B, W, dtype=torch.int32, device="cuda")
+    token, sc = torch.empty_like(parent), torch.empty(B, W, device="cuda")
+
+    def step():
+        sv.spec_beam_select(ctx, logits, score, None, parent, token, sc)
+        sv.spec_beam_reorder(parent, state, state)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    sv.spec_beam_set_stream(ctx, side)
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for n in range(5):
+        new, ns = make(B, W, V, "bf16", seed=20 + n)
+        logits.copy_(new)
+        score.copy_(ns)
+        state.copy_(torch.randn(L, B, W, S, device="cuda"))
+        before = state.cpu().numpy()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = select(logits, score, None, W, "bf16")
+        assert np.array_equal(parent.cpu().numpy(), eager[0])
+        assert np.array_equal(token.cpu().numpy(), eager[1])
+        assert np.array_equal(sc.cpu().numpy(), eager[2])
+        assert np.array_equal(state.cpu().numpy(), ops.beam_reorder(eager[0], before, before))
+
+
+def test_refusals_of_the_binding():
+    logits, score = make(2, 3, 100, "f32", seed=1)
+    ctx = sv.spec_beam_init(2, 3, 4, 100, torch.float32)
+    i, f = torch.empty(2, 4, dtype=torch.int32, device="cuda"), torch.empty(2, 4, device="cuda")
+    with pytest.raises(TypeError):
+        sv.spec_beam_select(ctx, logits.bfloat16(), score, None, i, i.clone(), f)
+    with pytest.raises(ValueError):
+        sv.spec_beam_select(ctx, logits[:, :, :99], score, None, i, i.clone(), f)
+    with pytest.raises(ValueError):
+        sv.spec_beam_select(ctx, logits.transpose(0, 1).contiguous().transpose(0, 1), score, None, i, i.clone(), f)
+    with pytest.raises(ValueError):
+        sv.spec_beam_select(ctx, logits, score.cpu(), None, i, i.clone(), f)
+    with pytest.raises(TypeError):
+        sv.spec_beam_select(ctx, logits, score, torch.zeros(2, 3, device="cuda"), i, i.clone(), f)
+
+
+# ------------------------------------------------------------------ reorder ---
+
+@pytest.mark.parametrize("L,B,W,K,shape,dtype", [
+    (1, 1, 1, 1, (1,), torch.int8),
+    (2, 3, 4, 4, (5,), torch.int8),          # single bytes
+    (3, 2, 5, 7, (3, 2), torch.float32),     # 4-byte columns
+    (2, 3, 4, 9, (6, 8), torch.bfloat16),
+    (1, 2, 16, 16, (1000,), torch.float32),
+    (2, 1, 33, 33, (130,), torch.int32),
+    (1, 2, 64, 64, (77, 4), torch.float32),
+    (1, 1, 64, 20, (4096,), torch.bfloat16),
+])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_reorder(L, B, W, K, shape, dtype, in_place):
+    K = W if in_place else K
+    g = torch.Generator().manual_seed(L + B + W + K)
+    rand = lambda n: torch.randint(-100, 100, (L, B, n, *shape), generator=g).to(dtype).cuda()
+    src, dst = rand(W), rand(K)
+    for kind in ("any", "same", "swap"):
+        parent = {"any": torch.randint(-1, W + 1, (B, K), generator=g),     # W lies outside
+                  "same": torch.arange(K).remainder(W).expand(B, K),
+                  "swap": (W - 1 - torch.arange(K).remainder(W)).expand(B, K)}[kind].int().cuda().contiguous()
+        a, b = src.clone(), dst.clone()
+        if in_place:
+            b = a
+        want = ops.beam_reorder(parent.cpu().numpy(), a.float().cpu().numpy(), b.float().cpu().numpy())
+        sv.spec_beam_reorder(parent, a, b)
+        torch.cuda.synchronize()
+        assert np.array_equal(b.float().cpu().numpy(), want), kind
+        if not in_place:
+            assert torch.equal(a, src)
+
+
+@pytest.mark.parametrize("used", [0, 1, 6, 8, 48, 64])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_reorder_moves_a_prefix(used, in_place):
+    g = torch.Generator().manual_seed(used)
+    src = torch.randint(-128, 128, (2, 3, 5, 64), generator=g, dtype=torch.int8).cuda()
+    dst = src if in_place else torch.randint(-128, 128, (2, 3, 5, 64), generator=g, dtype=torch.int8).cuda()
+    parent = torch.randint(-1, 5, (3, 5), generator=g).int().cuda()
+    old, before = src.cpu().numpy(), dst.cpu().numpy()
+    sv.spec_beam_reorder(parent, src, dst, used_bytes=used)
+    torch.cuda.synchronize()
+    want = before.copy()
+    want[..., :used] = ops.beam_reorder(parent.cpu().numpy(), old[..., :used], before[..., :used])
+    assert np.array_equal(dst.cpu().numpy(), want)
+
+
+def test_reorder_past_32_bit_offsets():
+    """States beyond 4 GiB from the start of their array."""
+    L, B, W, S = 3, 1, 3, 1 << 29
+    state = torch.zeros(L, B, W, S, dtype=torch.int8, device="cuda")
+    for l in range(L):
+        for w in range(W):
+            state[l, 0, w].fill_(10 * l + w)
+    parent = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    sv.spec_beam_reorder(parent, state, state)
+    for l in range(L):
+        for w, p in enumerate((2, 0, 1)):
+            assert bool((state[l, 0, w] == 10 * l + p).all())
+    del state
+    torch.cuda.empty_cache()
+
+
+def test_selection_past_32_bit_offsets():
+    """Rows that start more than 2^32 bytes behind the first."""
+    B, W, V = 9, 4, 40_000_000
+    logits = torch.zeros(B, W, V, dtype=torch.bfloat16, device="cuda")
+    logits[8, 3, V - 1] = 9.0
+    logits[8, 3, 5] = 8.0
+    logits[0, 1, 7] = 9.0
+    lse = torch.zeros(B, W, dtype=torch.float64, device="cuda")
+    score = torch.zeros(B, W, device="cuda")
+    p, t, s, q = select(logits, score, lse, 2, "bf16")
+    assert p[8].tolist() == [3, 3] and t[8].tolist() == [V - 1, 5] and s[8].tolist() == [9.0, 8.0]
+    assert p[0].tolist() == [1, 0] and t[0].tolist() == [7, 0]
+    assert p[4].tolist() == [0, 0] and t[4].tolist() == [0, 1]
+    del logits
+    torch.cuda.empty_cache()
