@@ -11,9 +11,9 @@
 //     while its K largest keys are found, so the logits are read once;
 //   beam_merge: one workgroup per sequence; forms the binary64 values of the
 //     pieces' keys and keeps the K best over the beams.
-// Both narrow by the K-th largest of their threads' largest entries (at least K
-// entries reach it, and few more do), collect what reaches it in LDS, and rank
-// the collected entries by counting. Collected in any order, ranked by a total
+// Both narrow by a bar from their threads' largest entries (at least K entries
+// reach it, and few more do), collect what reaches it in LDS, and rank the
+// collected entries by counting. Collected in any order, ranked by a total
 // order: the result does not depend on timing.
 #include <hip/hip_runtime.h>
 
@@ -76,22 +76,50 @@ __device__ inline T wave_sort(T v) {
     return v;
 }
 
-// The keep-th largest of the workgroup's values, one per thread (keep <= 64).
-// Every wavefront sorts its own; a thread's place in the whole is its place in
-// its own list plus the entries before it in the others. sorted: kWaves * 64
-// values of LDS, result: one. Equal values are placed by wavefront.
+// The keep-th largest of the maxima of the workgroup's runs of G lanes (kBlock
+// / G of them, at most 64): every wavefront ranks all of them by counting, so
+// one barrier does. lds: kBlock / G values.
+template <int G, typename T>
+__device__ inline T kth_of_groups(T v, int keep, T* lds) {
+    constexpr int N = kBlock / G;
+    static_assert(N <= 64, "one maximum per lane");
+#pragma unroll
+    for (int off = 1; off < G; off <<= 1) {
+        const T o = __shfl_xor(v, off, 64);
+        v = o > v ? o : v;
+    }
+    if (threadIdx.x % G == 0)
+        lds[threadIdx.x / G] = v;
+    __syncthreads();
+    const int i = (threadIdx.x & 63) % N;
+    v = lds[i];
+    int place = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const T o = lds[j];
+        place += o > v || (o == v && j < i);
+    }
+    const unsigned long long at = __ballot(place == keep - 1);
+    const int src = __ffsll(static_cast<long long>(at)) - 1;
+    return __shfl(v, src, 64);
+}
+
+// The keep-th largest of the threads' own values: every wavefront sorts its 64;
+// a thread's place in the whole is its place in its own list plus the entries
+// before it in the others (equal values are placed by wavefront). lds: kBlock
+// values and one more.
 template <typename T>
-__device__ inline T kth_largest(T v, int keep, T* sorted, T* result) {
+__device__ inline T kth_of_threads(T v, int keep, T* lds) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     v = wave_sort(v);
-    sorted[wid * 64 + lane] = v;
+    lds[wid * 64 + lane] = v;
     __syncthreads();
     int place = lane;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         if (w == wid)
             continue;
-        const T* list = sorted + w * 64;
+        const T* list = lds + w * 64;
         int lo = 0;  // entries of the list before v
 #pragma unroll
         for (int step = 64; step > 0; step >>= 1) {
@@ -102,9 +130,24 @@ __device__ inline T kth_largest(T v, int keep, T* sorted, T* result) {
         place += lo;
     }
     if (place == keep - 1)
-        *result = v;
+        lds[kBlock] = v;
     __syncthreads();
-    return *result;
+    return lds[kBlock];
+}
+
+// A bar that at least `keep` of the workgroup's entries reach (each thread
+// giving the largest of its own, `busy` threads having any), and few more: the
+// keep-th largest of 16 maxima over 16 threads lets about 1.4 keep (keep = 8)
+// to 3.4 keep (16) entries of evenly spread data through, of 64 maxima over
+// 4 threads 1.4 keep (32), of the threads' own 1.15 keep (64). The first
+// two cost a few lane exchanges and one barrier, the last a sort.
+template <typename T>
+__device__ inline T bar_of(T v, int keep, int busy, T* lds) {
+    if (keep <= 16 && busy >= 16 * keep)
+        return kth_of_groups<16>(v, keep, lds);
+    if (keep <= 32 && busy >= 4 * keep)
+        return kth_of_groups<4>(v, keep, lds);
+    return kth_of_threads(v, keep, lds);
 }
 
 __device__ inline uint64_t block_max_u64(uint64_t v, uint64_t* lds) {
@@ -122,6 +165,15 @@ __device__ inline uint64_t block_max_u64(uint64_t v, uint64_t* lds) {
     for (int w = 1; w < kWaves; ++w)
         v = lds[w] > v ? lds[w] : v;
     return v;
+}
+
+// Names the piece's registers, so that what was unpacked from them before is
+// unpacked again instead of being kept (64 registers against 32).
+template <int U>
+__device__ __forceinline__ void repack(uint4 (&q)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        asm volatile("" : "+v"(q[u].x), "+v"(q[u].y), "+v"(q[u].z), "+v"(q[u].w));
 }
 
 // The K largest keys of piece p of row `row`, largest first, 0 where the piece
@@ -150,26 +202,30 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
     uint4 q[U];
     r.template load<U, kBlock>(g0 + tid, g1, q);
 
-    __shared__ float sorted[kBlock];
-    __shared__ float kth;
+    __shared__ float bars[kBlock + 1];
     __shared__ uint64_t list[kCollect];
     __shared__ uint64_t lds64[kWaves];
+    __shared__ float lds_f[kWaves];
     __shared__ int count;
     if (tid == 0)
         count = 0;
 
     const float inf = __builtin_huge_valf();
+    float most[U];  // the largest of each group
     float best = -inf;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float z[W];
         Row::unpack(q[u], z);
+        most[u] = z[0];
 #pragma unroll
-        for (int e = 0; e < W; ++e)
-            best = fmaxf(best, z[e]);
+        for (int e = 1; e < W; ++e)
+            most[u] = fmaxf(most[u], z[e]);
+        best = fmaxf(best, most[u]);
     }
     if (best == inf) {  // an infinite logit is no candidate
         best = -inf;
+        repack(q);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float z[W];
@@ -179,13 +235,12 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
                 best = z[e] < inf ? fmaxf(best, z[e]) : best;
         }
     }
-    const float bar = kth_largest(best, keep, sorted, &kth);
+    const int held = g1 - g0;
+    const float bar = bar_of(best, keep, held < kBlock ? held : kBlock, bars);
 
+    repack(q);
     if constexpr (NORM) {
-        float m = sorted[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w)
-            m = fmaxf(m, sorted[w * 64]);
+        const float m = block_max(best, lds_f);
         const float ref = m == -inf ? 0.0f : m;
         double s = 0.0;
 #pragma unroll
@@ -205,9 +260,13 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
             norm[row * pieces + p] = NormPart{m, 0, s};
     }
 
+    repack(q);
     if (best >= bar && best > -inf) {
+        const int v0 = static_cast<int>(r.element(g0 + tid));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (!(most[u] >= bar))
+                continue;
             float z[W];
             Row::unpack(q[u], z);
 #pragma unroll
@@ -215,7 +274,7 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
                 if (z[e] >= bar && is_finite_f32(z[e])) {
                     const int slot = atomicAdd(&count, 1);
                     if (slot < kCollect)
-                        list[slot] = make_key(z[e], static_cast<int>(r.element(g0 + tid + u * kBlock) + e));
+                        list[slot] = make_key(z[e], v0 + u * kBlock * W + e);
                 }
             }
         }
@@ -236,18 +295,23 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
         return;
     }
     // More entries tie at the bar than the list holds: take the largest
-    // remaining key keep times. n > kCollect >= keep, so all keep exist.
+    // remaining key keep times, reading the piece again each time (its
+    // registers would be needed on top of the keys'). n > kCollect >= keep, so
+    // all keep exist.
     uint64_t last = ~0ull;
     for (int k = 0; k < keep; ++k) {
         uint64_t mine = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
+#pragma unroll 1
+        for (int g = g0 + tid; g < g1; g += kBlock) {
+            uint4 one[1];
+            r.template load<1, kBlock>(g, g1, one);
             float z[W];
-            Row::unpack(q[u], z);
+            Row::unpack(one[0], z);
+            const int v0 = static_cast<int>(r.element(g));
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 if (z[e] >= bar && is_finite_f32(z[e])) {
-                    const uint64_t key = make_key(z[e], static_cast<int>(r.element(g0 + tid + u * kBlock) + e));
+                    const uint64_t key = make_key(z[e], v0 + e);
                     mine = key < last && key > mine ? key : mine;
                 }
             }
@@ -281,8 +345,7 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(
     int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
     __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
     __shared__ int alive[SPEC_BEAM_MAX];
-    __shared__ uint64_t sorted[kBlock];
-    __shared__ uint64_t kth;
+    __shared__ uint64_t bars[kBlock + 1];
     __shared__ Cand list[kCollect];
     __shared__ Cand wave_best[kWaves];
     __shared__ int count;
@@ -337,7 +400,7 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(
         const uint64_t v = candidate(c).value;
         best = v > best ? v : best;
     }
-    const uint64_t bar = kth_largest(best, keep, sorted, &kth);
+    const uint64_t bar = bar_of(best, keep, total < kBlock ? total : kBlock, bars);
     if (best >= bar && best != 0) {
         for (int c = tid; c < total; c += kBlock) {
             const Cand x = candidate(c);

@@ -80,13 +80,23 @@ struct RowGroups {
                 q[u] = make_uint4(v.x, v.y, v.z, v.w);
             }
         }
+        // The groups at the row's ends: the first can only be this thread's
+        // first, the last any one of its groups.
+        const int tail = groups - 1;
+        const bool has_tail = !inside(tail) && tail >= g0 && tail < end && (tail - g0) % STEP == 0 &&
+                              tail - g0 < U * STEP;
+        uint4 last = neg_inf();
+        if (has_tail)
+            last = load_end(tail);
+        if (g0 == 0 && end > 0 && tail > 0 && !inside(0))
+            q[0] = load_end(0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int g = g0 + u * STEP;
             if (g >= end)
                 q[u] = neg_inf();
-            else if (!inside(g))
-                q[u] = load_end(g);
+            else if (has_tail && g == tail)
+                q[u] = last;
         }
     }
 
