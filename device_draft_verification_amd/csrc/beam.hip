@@ -150,23 +150,6 @@ __device__ inline T bar_of(T v, int keep, int busy, T* lds) {
     return kth_of_threads(v, keep, lds);
 }
 
-__device__ inline uint64_t block_max_u64(uint64_t v, uint64_t* lds) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const uint64_t o = __shfl_xor(static_cast<unsigned long long>(v), off, 64);
-        v = o > v ? o : v;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w)
-        v = lds[w] > v ? lds[w] : v;
-    return v;
-}
-
 // Names the piece's registers, so that what was unpacked from them before is
 // unpacked again instead of being kept (64 registers against 32).
 template <int U>
@@ -260,65 +243,57 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
             norm[row * pieces + p] = NormPart{m, 0, s};
     }
 
-    repack(q);
-    if (best >= bar && best > -inf) {
-        const int v0 = static_cast<int>(r.element(g0 + tid));
+    // Collect the entries that reach the bar. If the list overflows (ties at the
+    // bar, or a vocabulary whose best entries lie together), the keep-th largest
+    // key that did fit is a higher bar, and keys are unique: again with that.
+    float bar_z = bar;
+    uint64_t bar_key = 0;
+    int v0 = static_cast<int>(r.element(g0 + tid));
+    for (;;) {
+        repack(q);
+        asm volatile("" : "+v"(v0));  // nor the 64 tokens over the loop
+        if (best >= bar_z && best > -inf) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!(most[u] >= bar))
-                continue;
-            float z[W];
-            Row::unpack(q[u], z);
+            for (int u = 0; u < U; ++u) {
+                if (!(most[u] >= bar_z))
+                    continue;
+                float z[W];
+                Row::unpack(q[u], z);
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                if (z[e] >= bar && is_finite_f32(z[e])) {
-                    const int slot = atomicAdd(&count, 1);
-                    if (slot < kCollect)
-                        list[slot] = make_key(z[e], v0 + u * kBlock * W + e);
+                for (int e = 0; e < W; ++e) {
+                    const uint64_t key = make_key(z[e], v0 + u * kBlock * W + e);
+                    if (z[e] >= bar_z && is_finite_f32(z[e]) && key >= bar_key) {
+                        const int slot = atomicAdd(&count, 1);
+                        if (slot < kCollect)
+                            list[slot] = key;
+                    }
                 }
             }
         }
-    }
-    __syncthreads();
-    const int n = count;
-    if (n <= kCollect) {
-        if (tid < n) {
-            const uint64_t mine = list[tid];
-            int place = 0;
-            for (int i = 0; i < n; ++i)
-                place += list[i] > mine;
-            if (place < keep)
-                out[place] = mine;
-        } else if (tid < keep) {
-            out[tid] = 0;
-        }
-        return;
-    }
-    // More entries tie at the bar than the list holds: take the largest
-    // remaining key keep times, reading the piece again each time (its
-    // registers would be needed on top of the keys'). n > kCollect >= keep, so
-    // all keep exist.
-    uint64_t last = ~0ull;
-    for (int k = 0; k < keep; ++k) {
-        uint64_t mine = 0;
-#pragma unroll 1
-        for (int g = g0 + tid; g < g1; g += kBlock) {
-            uint4 one[1];
-            r.template load<1, kBlock>(g, g1, one);
-            float z[W];
-            Row::unpack(one[0], z);
-            const int v0 = static_cast<int>(r.element(g));
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                if (z[e] >= bar && is_finite_f32(z[e])) {
-                    const uint64_t key = make_key(z[e], v0 + e);
-                    mine = key < last && key > mine ? key : mine;
-                }
+        __syncthreads();
+        const int n = count;
+        const int held_keys = n < kCollect ? n : kCollect;
+        const uint64_t mine = tid < held_keys ? list[tid] : 0;
+        int place = 0;
+        for (int i = 0; i < held_keys; ++i)
+            place += list[i] > mine;
+        if (n <= kCollect) {
+            if (tid < n) {
+                if (place < keep)
+                    out[place] = mine;
+            } else if (tid < keep) {
+                out[tid] = 0;
             }
+            return;
         }
-        last = block_max_u64(mine, lds64);
+        if (place == keep - 1)
+            lds64[0] = mine;
+        __syncthreads();
+        bar_key = lds64[0];
+        bar_z = key_logit(bar_key);
         if (tid == 0)
-            out[k] = last;
+            count = 0;
+        __syncthreads();
     }
 }
 
@@ -344,10 +319,10 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(
     int pieces, const uint64_t* __restrict__ keys, const NormPart* __restrict__ norm,
     int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
     __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
-    __shared__ int alive[SPEC_BEAM_MAX];
+    __shared__ int alive[SPEC_BEAM_MAX], live[SPEC_BEAM_MAX], live_count;
     __shared__ uint64_t bars[kBlock + 1];
     __shared__ Cand list[kCollect];
-    __shared__ Cand wave_best[kWaves];
+    __shared__ Cand next_bar;
     __shared__ int count;
     const long b = blockIdx.x;
     const int tid = threadIdx.x;
@@ -384,35 +359,40 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(
         alive[w] = ok;
     }
     __syncthreads();
-
-    const int per_beam = pieces * keep, total = beams * per_beam;
-    const uint64_t* k_b = keys + b * total;
-    auto candidate = [&](int c) {
-        const int w = c / per_beam;
-        const uint64_t key = k_b[c];
+    if (tid < 64) {  // the live beams, in order (at most 64)
+        const bool on = tid < beams && alive[tid];
+        const unsigned long long mask = __ballot(on);
+        if (on)
+            live[__popcll(mask & ((1ull << tid) - 1))] = tid;
+        if (tid == 0)
+            live_count = __popcll(mask);
+    }
+    __syncthreads();
+    // The live beams' lists, one per piece, sorted: `share` threads to a list,
+    // thread (l, r) taking its entries r, r + share, ... The first of them is the
+    // thread's largest.
+    const int n_live = live_count;
+    const int lists = n_live * pieces;
+    const int share = lists < kBlock ? kBlock / (lists > 0 ? lists : 1) : 1;
+    const int step = kBlock / share;  // lists taken at a time
+    const uint64_t* k_b = keys + b * beams * pieces * keep;
+    auto candidate = [&](int l, int r) {
+        const int w = live[l / pieces];
+        const uint64_t key = k_b[(static_cast<long>(w) * pieces + l % pieces) * keep + r];
         Cand x{0, key, w};
-        if (key != 0 && alive[w])
+        if (key != 0)
             x.value = ordered64(b_score[w] + (static_cast<double>(key_logit(key)) - b_lse[w]));
         return x;
     };
+    const int l0 = tid / share, r0 = tid % share;
     uint64_t best = 0;
-    for (int c = tid; c < total; c += kBlock) {
-        const uint64_t v = candidate(c).value;
-        best = v > best ? v : best;
-    }
-    const uint64_t bar = bar_of(best, keep, total < kBlock ? total : kBlock, bars);
-    if (best >= bar && best != 0) {
-        for (int c = tid; c < total; c += kBlock) {
-            const Cand x = candidate(c);
-            if (x.value >= bar && x.value != 0) {
-                const int slot = atomicAdd(&count, 1);
-                if (slot < kCollect)
-                    list[slot] = x;
-            }
+    if (r0 < keep && l0 < step)
+        for (int l = l0; l < lists; l += step) {
+            const uint64_t v = candidate(l, r0).value;
+            best = v > best ? v : best;
         }
-    }
-    __syncthreads();
-    const int n = count;
+    const uint64_t first_bar = keep <= 32 ? kth_of_groups<4>(best, keep, bars) : kth_of_threads(best, keep, bars);
+    Cand bar{first_bar, 0, SPEC_BEAM_MAX};  // behind every candidate of that value
     auto emit = [&](int j, const Cand& x) {
         const long at = b * keep + j;
         const bool some = x.value != 0;
@@ -423,47 +403,42 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(
             out_logq[at] = some ? static_cast<float>(static_cast<double>(key_logit(x.key)) - b_lse[x.beam])
                                 : -__builtin_huge_valf();
     };
-    if (n <= kCollect) {
-        if (tid < n) {
-            const Cand mine = list[tid];
-            int place = 0;
-            for (int i = 0; i < n; ++i)
-                place += before(list[i], mine);
-            if (place < keep)
-                emit(place, mine);
-        } else if (tid < keep) {
-            emit(tid, Cand{0, 0, 0});
-        }
-        return;
-    }
-    // More ties than the list holds: the best remaining candidate, keep times.
-    Cand last{~0ull, ~0ull, -1};
-    for (int k = 0; k < keep; ++k) {
-        Cand mine{0, 0, 0};
-        for (int c = tid; c < total; c += kBlock) {
-            const Cand x = candidate(c);
-            if (x.value != 0 && before(last, x) && (mine.value == 0 || before(x, mine)))
-                mine = x;
-        }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            Cand o;
-            o.value = __shfl_xor(static_cast<unsigned long long>(mine.value), off, 64);
-            o.key = __shfl_xor(static_cast<unsigned long long>(mine.key), off, 64);
-            o.beam = __shfl_xor(mine.beam, off, 64);
-            if (o.value != 0 && (mine.value == 0 || before(o, mine)))
-                mine = o;
+    for (;;) {
+        if (r0 < keep && l0 < step && best != 0 && best >= bar.value) {
+            for (int l = l0; l < lists; l += step)
+                for (int r = r0; r < keep; r += share) {
+                    const Cand x = candidate(l, r);
+                    if (x.value == 0 || before(bar, x))
+                        break;  // sorted: nothing further of this list
+                    const int slot = atomicAdd(&count, 1);
+                    if (slot < kCollect)
+                        list[slot] = x;
+                }
         }
         __syncthreads();
-        if ((tid & 63) == 0)
-            wave_best[tid >> 6] = mine;
+        const int n = count;
+        const int held = n < kCollect ? n : kCollect;
+        const Cand mine = tid < held ? list[tid] : Cand{0, 0, SPEC_BEAM_MAX};
+        int place = 0;
+        for (int i = 0; i < held; ++i)
+            place += before(list[i], mine);
+        if (n <= kCollect) {
+            if (tid < n) {
+                if (place < keep)
+                    emit(place, mine);
+            } else if (tid < keep) {
+                emit(tid, Cand{0, 0, 0});
+            }
+            return;
+        }
+        // Overflow: the keep-th best of those that fit is a higher bar.
+        if (place == keep - 1)
+            next_bar = mine;
         __syncthreads();
-        last = wave_best[0];
-        for (int w = 1; w < kWaves; ++w)
-            if (wave_best[w].value != 0 && (last.value == 0 || before(wave_best[w], last)))
-                last = wave_best[w];
+        bar = next_bar;
         if (tid == 0)
-            emit(k, last);
+            count = 0;
+        __syncthreads();
     }
 }
 

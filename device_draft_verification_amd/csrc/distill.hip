@@ -4,10 +4,17 @@
 //   loss = sum_j p_j (log p_j - (x_id(j) - lse)),
 //   grad_v = weight / T (P exp(x_v - lse) - sum_{j: id(j) = v} p_j).
 //
-// One workgroup per row. The dense part of the gradient is written first; a
-// barrier later the entries of the list, whose students' logits were fetched
-// before anything was written, overwrite their places (so the gradient may
-// take the logits' place, and no element is rounded twice).
+// Three kernels:
+//   distill_forward: one workgroup per row streams it once;
+//   distill_backward: a row's groups are split over workgroups (nothing is
+//     summed over the vocabulary);
+//   distill_loss_grad: one workgroup per row keeps the row in registers between
+//     its normaliser and its gradient, so that the logits are read once (rows
+//     that do not fit are read twice).
+// The dense part of the gradient is written first; a barrier later the entries
+// of the list, whose students' logits were fetched before anything was
+// written, overwrite their places (so the gradient may take the logits' place,
+// and no element is rounded twice).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -18,10 +25,6 @@
 
 namespace specv {
 namespace {
-
-constexpr int kThreads = 1024;
-constexpr int kRowWaves = kThreads / 64;
-constexpr int kUnroll = 4;
 
 struct DistillArgs {
     const void* logits;
@@ -37,37 +40,180 @@ struct DistillArgs {
     int vocab, top_k;
 };
 
-struct ListEntry {
-    int id;       // -1: unused
-    float x;      // the student's scaled logit there
-    double p;     // the teacher's probability
+// ----------------------------------------------------------------- the list ---
+
+// A row's teacher list after reduction, the same in every thread.
+struct RowList {
+    bool empty;    // nothing to learn: loss and gradient 0
+    bool bad;      // loss and gradient NaN
+    float inv_t;
+    double mass;   // P
+    double inner;  // sum_j p_j (log p_j - x_id(j)), so that loss = inner + P lse
 };
 
-__device__ inline double row_sum(double v, double* lds) {
-    v = wave_sum(v);
+// A thread's own entry (threads past the list hold none).
+struct Entry {
+    int id;    // -1: unused
+    float x;   // the student's scaled logit there
+    double p;  // the teacher's probability
+};
+
+struct ListLds {
+    int id[SPEC_DISTILL_MAX_K];
+    double p[SPEC_DISTILL_MAX_K];
+    float most[4];
+    int flags[4];
+    double sum[4], inner[4];
+};
+
+// With e_j = exp(y_j - m): over the list (teacher_lse NULL, m its largest y)
+// p_j = e_j / S and log p_j = y_j - m - log S, S = sum e; so sum p (log p - x)
+// = T / S - log S with T = sum e (y - m - x): S and T in one exchange. With
+// the teacher's own normaliser as m, p = e, P = S and the sum is T.
+template <int DT>
+__device__ inline RowList reduce_list(const DistillArgs& a, long row, const RowGroups<DT>& r,
+                                      Entry& mine, ListLds& lds) {
+    const int tid = threadIdx.x, wid = tid >> 6;
+    const float inf = __builtin_huge_valf();
+    RowList out{};
+    const bool t_ok = temperature_mode(a.temperature[row], &out.inv_t) == 1;
+    mine = Entry{-1, 0.0f, 0.0};
+    float y = -inf;
+    if (tid < a.top_k) {
+        const int id = a.ids[row * a.top_k + tid];
+        if (id >= 0) {
+            mine.id = id;
+            y = a.teacher[row * a.top_k + tid] * out.inv_t;
+            if (id < a.vocab)
+                mine.x = r.at(id) * out.inv_t;
+        }
+    }
+    if (tid < SPEC_DISTILL_MAX_K) {
+        const bool used = mine.id >= 0;
+        const bool any_used = __ballot(used) != 0, any_out = __ballot(used && mine.id >= a.vocab) != 0,
+                   any_mass = __ballot(used && !(y == -inf)) != 0;
+        const float m = wave_max(y);
+        if ((tid & 63) == 0) {
+            lds.most[wid] = m;
+            lds.flags[wid] = (any_used ? 1 : 0) | (any_out ? 2 : 0) | (any_mass ? 4 : 0);
+        }
+    }
     __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
+    const int flags = lds.flags[0] | lds.flags[1] | lds.flags[2] | lds.flags[3];
+    const bool own_norm = a.teacher_lse != nullptr;
+    out.bad = !t_ok || (flags & 2);
+    out.empty = !(flags & 1) || (!out.bad && !own_norm && !(flags & 4));
+    const double m = own_norm ? a.teacher_lse[row]
+                              : static_cast<double>(fmaxf(fmaxf(lds.most[0], lds.most[1]),
+                                                          fmaxf(lds.most[2], lds.most[3])));
+    double e = 0.0;
+    if (tid < SPEC_DISTILL_MAX_K) {
+        double t = 0.0;
+        if (mine.id >= 0) {
+            const double d = static_cast<double>(y) - m;
+            e = exp(d);
+            if (!(e == 0.0))
+                t = e * (d - static_cast<double>(mine.x));
+        }
+        const double s = wave_sum(e), w = wave_sum(t);
+        if ((tid & 63) == 0) {
+            lds.sum[wid] = s;
+            lds.inner[wid] = w;
+        }
+    }
     __syncthreads();
-    double s = lds[0];
-#pragma unroll
-    for (int w = 1; w < kRowWaves; ++w)
-        s += lds[w];
-    return s;
+    const double s = (lds.sum[0] + lds.sum[1]) + (lds.sum[2] + lds.sum[3]);
+    const double t = (lds.inner[0] + lds.inner[1]) + (lds.inner[2] + lds.inner[3]);
+    out.bad = out.bad || !is_finite_f64(m) || !is_finite_f64(s);
+    out.mass = own_norm ? s : 1.0;
+    out.inner = own_norm ? t : t / s - log(s);
+    mine.p = own_norm ? e : e / s;
+    if (tid < a.top_k) {
+        lds.id[tid] = mine.id;
+        lds.p[tid] = mine.p;
+    }
+    return out;
 }
 
-__device__ inline float row_max(float v, float* lds) {
-    v = wave_max(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float m = lds[0];
+// ---------------------------------------------------------- the normaliser ---
+
+// Running (ref, s) of a thread, s = sum 2^(x log2e - ref): a batch is summed
+// against the current reference, and only where that passes 2^8 a group the
+// reference is moved to the batch's maximum first. Terms then stay within 2^8
+// of 1, so the rounding of their exponents grows by at most 8 steps of 2^-24.
+constexpr float kLazy = 256.0f;
+
+template <int DT>
+__device__ inline float group_sum(const uint4& q, float inv_t, float ref) {
+    constexpr int W = RowGroups<DT>::W;
+    float z[W], t[W];
+    RowGroups<DT>::unpack(q, z);
 #pragma unroll
-    for (int w = 1; w < kRowWaves; ++w)
-        m = fmaxf(m, lds[w]);
+    for (int e = 0; e < W; ++e)
+        t[e] = fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -ref));
+#pragma unroll
+    for (int n = W / 2; n > 0; n >>= 1)
+#pragma unroll
+        for (int e = 0; e < n; ++e)
+            t[e] += t[e + n];
+    return t[0];
+}
+
+template <int DT>
+__device__ inline float group_max(const uint4& q) {
+    constexpr int W = RowGroups<DT>::W;
+    float z[W];
+    RowGroups<DT>::unpack(q, z);
+    float m = z[0];
+#pragma unroll
+    for (int e = 1; e < W; ++e)
+        m = fmaxf(m, z[e]);
     return m;
 }
+
+template <int DT>
+__device__ __forceinline__ void online_add(const uint4& q, float inv_t, float& ref, double& s) {
+    float g = group_sum<DT>(q, inv_t, ref);
+    if (!(g <= kLazy)) {
+        const float next = fmaxf(ref, scale_logit(group_max<DT>(q), inv_t) * kLog2e);
+        s *= static_cast<double>(fast_exp2(ref - next));
+        ref = next;
+        g = group_sum<DT>(q, inv_t, ref);
+    }
+    s += static_cast<double>(g);
+}
+
+// The first reference: the wavefront's largest entry of its first groups, or
+// none (kNegMax) where those hold nothing finite.
+template <int DT>
+__device__ __forceinline__ float first_reference(const uint4& q, float inv_t) {
+    return fmaxf(kNegMax, scale_logit(wave_max(group_max<DT>(q)), inv_t) * kLog2e);
+}
+
+// lse * log2e of the row from the threads' pairs. lds: 2 values per wavefront.
+template <int WAVES>
+__device__ inline double join(float ref, double s, double* lds) {
+    const float m = wave_max(ref);
+    s = wave_sum(s * static_cast<double>(ref == m ? 1.0f : fast_exp2(ref - m)));
+    if ((threadIdx.x & 63) == 0) {
+        lds[2 * (threadIdx.x >> 6)] = static_cast<double>(m);
+        lds[2 * (threadIdx.x >> 6) + 1] = s;
+    }
+    __syncthreads();
+    double top = lds[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w)
+        top = fmax(top, lds[2 * w]);
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const float d = static_cast<float>(lds[2 * w] - top);
+        sum += lds[2 * w + 1] * static_cast<double>(fast_exp2(d));
+    }
+    return top + log2(sum);
+}
+
+// ------------------------------------------------------------ the gradient ---
 
 template <int DT>
 __device__ inline void store_element(void* row, long v, float g) {
@@ -108,173 +254,247 @@ __device__ inline void store_group(const RowGroups<DT>& r, char* out, int g, boo
             store_element<DT>(out, e0 + i, d[i]);
 }
 
-template <int DT, bool LOSS, bool GRAD>
-__global__ __launch_bounds__(kThreads) void distill_kernel(DistillArgs a) {
+// The row's coefficients: exp(x - lse) = 2^(x log2e - ref) * 2^(ref - lse log2e),
+// the second factor (within a step of ref of 1) taken into the coefficient.
+struct GradScale {
+    float ref, dense;
+    double coef;
+};
+
+__device__ inline GradScale grad_scale(float weight, const RowList& l, double lse2) {
+    GradScale g;
+    g.ref = static_cast<float>(lse2);
+    g.coef = static_cast<double>(weight) * static_cast<double>(l.inv_t);
+    g.dense = static_cast<float>(g.coef * l.mass * exp2(static_cast<double>(g.ref) - lse2));
+    return g;
+}
+
+template <int DT>
+__device__ __forceinline__ void grad_group(const RowGroups<DT>& r, char* out, int g, bool whole,
+                                           const uint4& q, float inv_t, const GradScale& c) {
+    constexpr int W = RowGroups<DT>::W;
+    float z[W], d[W];
+    RowGroups<DT>::unpack(q, z);
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+        d[e] = c.dense * fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -c.ref));
+    store_group<DT>(r, out, g, whole, d);
+}
+
+template <int DT, int THREADS>
+__device__ inline void fill(const RowGroups<DT>& r, char* out, int g0, int g1, bool whole, float v) {
+    float d[RowGroups<DT>::W];
+#pragma unroll
+    for (int e = 0; e < RowGroups<DT>::W; ++e)
+        d[e] = v;
+    for (int g = g0 + static_cast<int>(threadIdx.x); g < g1; g += THREADS)
+        store_group<DT>(r, out, g, whole, d);
+}
+
+// The listed places, after the dense part: the first entry of an id writes the
+// sum over all entries of that id.
+template <int DT>
+__device__ inline void grad_list(const DistillArgs& a, const RowList& l, const Entry& mine,
+                                 const ListLds& lds, double lse, const GradScale& c, char* out) {
+    double sum = 0.0;
+    bool first = true;
+    for (int j = 0; j < a.top_k; ++j) {
+        if (lds.id[j] == mine.id) {
+            sum += lds.p[j];
+            first = first && j >= static_cast<int>(threadIdx.x);
+        }
+    }
+    if (first) {
+        const double q = exp(static_cast<double>(mine.x) - lse);
+        store_element<DT>(out, mine.id, static_cast<float>(c.coef * (l.mass * q - sum)));
+    }
+}
+
+template <int DT>
+__device__ inline char* grad_row(const DistillArgs& a, long row, const RowGroups<DT>& r, bool* whole) {
+    char* out = static_cast<char*>(a.out_grad) + row * static_cast<long>(a.vocab) * RowGroups<DT>::ESZ;
+    *whole = (reinterpret_cast<uintptr_t>(out) & 15) == static_cast<uintptr_t>(r.shift) * RowGroups<DT>::ESZ;
+    return out;
+}
+
+// ----------------------------------------------------------------- kernels ---
+
+template <int DT, int THREADS, int U>
+__global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a) {
     using Row = RowGroups<DT>;
-    constexpr int W = Row::W;
-    __shared__ ListEntry list[SPEC_DISTILL_MAX_K];
-    __shared__ double lds_d[kRowWaves];
-    __shared__ float lds_f[kRowWaves];
+    __shared__ ListLds list;
+    __shared__ double lds[2 * THREADS / 64];
     const int tid = threadIdx.x;
     const long row = blockIdx.x;
-    const float inf = __builtin_huge_valf();
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
-    char* out = GRAD ? static_cast<char*>(a.out_grad) + row * static_cast<long>(a.vocab) * Row::ESZ : nullptr;
-    const bool whole = GRAD && (reinterpret_cast<uintptr_t>(out) & 15) == static_cast<uintptr_t>(r.shift) * Row::ESZ;
-
-    // The list: the teacher's probabilities and the student's logits there.
-    float inv_t = 0.0f;
-    const bool t_ok = temperature_mode(a.temperature[row], &inv_t) == 1;
-    int id = -1;
-    float y = -inf;
-    if (tid < a.top_k) {
-        id = a.ids[row * a.top_k + tid];
-        if (id >= 0)
-            y = a.teacher[row * a.top_k + tid] * inv_t;
-        else
-            id = -1;
-    }
-    const bool used = id >= 0;
-    const bool outside = id >= a.vocab;
-    float x_id = 0.0f;
-    if (used && !outside)
-        x_id = r.at(id) * inv_t;
-    const bool any_used = __syncthreads_or(used);
-    const bool any_outside = __syncthreads_or(outside);
-    const bool any_mass = __syncthreads_or(used && !(y == -inf));
-    auto fill = [&](float v) {
-        if constexpr (GRAD) {
-            float d[W];
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                d[e] = v;
-            for (int g = tid; g < r.groups; g += kThreads)
-                store_group<DT>(r, out, g, whole, d);
-        }
-    };
+    uint4 q[U];
+    r.template load<U, THREADS>(tid, r.groups, q);
+    Entry mine;
+    const RowList l = reduce_list<DT>(a, row, r, mine, list);
     const float nan = __builtin_nanf("");
-    if (!any_used || (t_ok && !any_outside && !any_mass && !a.teacher_lse)) {
-        fill(0.0f);
-        if (LOSS && tid == 0) {
-            a.out_loss[row] = 0.0f;
-            a.out_lse[row] = nan;
+    if (l.empty || l.bad) {
+        if (tid == 0) {
+            a.out_loss[row] = l.empty ? 0.0f : nan;
+            a.out_lse[row] = static_cast<double>(nan);
         }
         return;
     }
-    double lse_t;
-    if (a.teacher_lse) {
-        lse_t = a.teacher_lse[row];
-    } else {
-        const float m = row_max(y, lds_f);
-        const double s = row_sum(used ? exp(static_cast<double>(y) - static_cast<double>(m)) : 0.0, lds_d);
-        lse_t = static_cast<double>(m) + log(s);
+    float ref = first_reference<DT>(q[0], l.inv_t);
+    double s = 0.0;
+    for (int g0 = tid;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            online_add<DT>(q[u], l.inv_t, ref, s);
+        g0 += U * THREADS;
+        if (g0 - tid >= r.groups)
+            break;
+        r.template load<U, THREADS>(g0, r.groups, q);
     }
-    bool bad = !t_ok || any_outside || !is_finite_f64(lse_t);
-    const double logp = static_cast<double>(y) - lse_t;
-    const double p = used ? exp(logp) : 0.0;
-    const double mass = row_sum(p, lds_d);
-    if (tid < a.top_k)
-        list[tid] = ListEntry{id, x_id, p};
+    const double lse = join<THREADS / 64>(ref, s, lds) / static_cast<double>(kLog2e);
+    if (tid == 0) {
+        const bool ok = is_finite_f64(lse);
+        a.out_loss[row] = ok ? static_cast<float>(l.inner + l.mass * lse) : nan;
+        a.out_lse[row] = ok ? lse : static_cast<double>(nan);
+    }
+}
 
-    // The row's normaliser: s = sum 2^(x log2e - m), log-normaliser in base-2
-    // units of the rounded constant, as the verifier keeps it.
-    float m = 0.0f;
-    double lse2 = 0.0;  // lse * kLog2e
-    if constexpr (LOSS) {
-        float mx = -inf;
-        double s = 0.0;
-        if (!bad) {
-            float ref = kNegMax;
-            for (int g0 = tid; g0 - tid < r.groups; g0 += kUnroll * kThreads) {
-                uint4 q[kUnroll];
-                r.template load<kUnroll, kThreads>(g0, r.groups, q);
-                float bm = -inf;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    float z[W];
-                    Row::unpack(q[u], z);
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        bm = fmaxf(bm, z[e]);
-                }
-                const float nr = fmaxf(ref, scale_logit(bm, inv_t) * kLog2e);
-                s *= nr == ref ? 1.0 : static_cast<double>(fast_exp2(ref - nr));
-                ref = nr;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    float z[W];
-                    Row::unpack(q[u], z);
-                    float gs = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        gs += fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -ref));
-                    s += static_cast<double>(gs);
-                }
-            }
-            mx = ref;
-        }
-        m = row_max(mx, lds_f);
-        s = row_sum(bad ? 0.0 : s * static_cast<double>(mx == m ? 1.0f : fast_exp2(mx - m)), lds_d);
-        lse2 = static_cast<double>(m) + log2(s);
-    } else {
-        lse2 = a.lse_in[row] * static_cast<double>(kLog2e);
+template <int DT, int THREADS, int U>
+__global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a, int splits) {
+    using Row = RowGroups<DT>;
+    __shared__ ListLds list;
+    const int tid = threadIdx.x;
+    const long row = blockIdx.x / static_cast<unsigned>(splits);
+    const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(splits));
+    const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
+    const int g0 = static_cast<int>(static_cast<long>(r.groups) * part / splits);
+    const int g1 = static_cast<int>(static_cast<long>(r.groups) * (part + 1) / splits);
+    bool whole;
+    char* out = grad_row<DT>(a, row, r, &whole);
+    uint4 q[U];
+    r.template load<U, THREADS>(g0 + tid, g1, q);
+    Entry mine;
+    const RowList l = reduce_list<DT>(a, row, r, mine, list);
+    const double lse = a.lse_in[row];
+    if (l.empty || l.bad || !is_finite_f64(lse)) {
+        fill<DT, THREADS>(r, out, g0, g1, whole, l.empty ? 0.0f : __builtin_nanf(""));
+        return;
     }
-    const double lse = LOSS ? lse2 / static_cast<double>(kLog2e) : a.lse_in[row];
-    bad = bad || !is_finite_f64(lse);
-    if constexpr (LOSS) {
-        double term = 0.0;
-        if (!bad && p > 0.0)
-            term = p * (logp - (static_cast<double>(x_id) - lse));
-        term = row_sum(term, lds_d);
-        if (tid == 0) {
-            a.out_loss[row] = bad ? nan : static_cast<float>(term);
-            a.out_lse[row] = bad ? static_cast<double>(nan) : lse;
-        }
+    const GradScale c = grad_scale(a.weight[row], l, lse * static_cast<double>(kLog2e));
+    for (int g = g0 + tid;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (g + u * THREADS < g1)
+                grad_group<DT>(r, out, g + u * THREADS, whole, q[u], l.inv_t, c);
+        g += U * THREADS;
+        if (g - tid >= g1)
+            break;
+        r.template load<U, THREADS>(g, g1, q);
     }
-    if constexpr (GRAD) {
-        if (bad) {
-            fill(nan);
-            return;
-        }
-        // exp(x - lse) = 2^(x log2e - ref) * 2^(ref - lse log2e), the second
-        // factor (below 1 step of ref from 1) taken into the row's coefficient.
-        const float ref = static_cast<float>(lse2);
-        const double coef = static_cast<double>(a.weight[row]) * static_cast<double>(inv_t);
-        const double dense = coef * mass * exp2(static_cast<double>(ref) - lse2);
-        const float df = static_cast<float>(dense);
-        __syncthreads();  // the list is written, and every gathered logit read
-        for (int g0 = tid; g0 - tid < r.groups; g0 += kUnroll * kThreads) {
-            uint4 q[kUnroll];
-            r.template load<kUnroll, kThreads>(g0, r.groups, q);
+    __syncthreads();  // the dense part is written
+    if (mine.id >= 0) {
+        const long at = (mine.id + r.shift) / Row::W;
+        if (at >= g0 && at < g1)
+            grad_list<DT>(a, l, mine, list, lse, c, out);
+    }
+}
+
+// R > 0: the row's groups, at most R * THREADS, stay in registers. R = 0: they
+// are read again for the gradient.
+template <int DT, int THREADS, int R>
+__global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs a) {
+    using Row = RowGroups<DT>;
+    constexpr int U = R ? R : 4;
+    __shared__ ListLds list;
+    __shared__ double lds[2 * THREADS / 64];
+    const int tid = threadIdx.x;
+    const long row = blockIdx.x;
+    const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
+    bool whole;
+    char* out = grad_row<DT>(a, row, r, &whole);
+    uint4 q[U];
+    r.template load<U, THREADS>(tid, r.groups, q);
+    Entry mine;
+    const RowList l = reduce_list<DT>(a, row, r, mine, list);
+    const float nan = __builtin_nanf("");
+    float ref = kNegMax;
+    double s = 0.0;
+    if (!l.empty && !l.bad) {
+        ref = first_reference<DT>(q[0], l.inv_t);
+        for (int g0 = tid;;) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (g0 + u * kThreads >= r.groups)
-                    break;
-                float z[W], d[W];
-                Row::unpack(q[u], z);
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    d[e] = df * fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -ref));
-                store_group<DT>(r, out, g0 + u * kThreads, whole, d);
-            }
-        }
-        __syncthreads();  // the dense part is written
-        if (tid < a.top_k && used) {
-            // The first entry of an id writes the sum of all entries of that id.
-            double sum = 0.0;
-            bool first = true;
-            for (int j = 0; j < a.top_k; ++j) {
-                if (list[j].id == id) {
-                    sum += list[j].p;
-                    first = first && j >= tid;
-                }
-            }
-            if (first) {
-                const double q = exp(static_cast<double>(x_id) - lse);
-                store_element<DT>(out, id, static_cast<float>(coef * (mass * q - sum)));
-            }
+            for (int u = 0; u < U; ++u)
+                online_add<DT>(q[u], l.inv_t, ref, s);
+            g0 += U * THREADS;
+            if (R || g0 - tid >= r.groups)
+                break;
+            r.template load<U, THREADS>(g0, r.groups, q);
         }
     }
+    const double lse2 = join<THREADS / 64>(ref, s, lds);
+    const double lse = lse2 / static_cast<double>(kLog2e);
+    const bool bad = l.bad || !is_finite_f64(lse);
+    if (tid == 0) {
+        a.out_loss[row] = l.empty ? 0.0f : bad ? nan : static_cast<float>(l.inner + l.mass * lse);
+        a.out_lse[row] = l.empty || bad ? static_cast<double>(nan) : lse;
+    }
+    if (l.empty || bad) {
+        fill<DT, THREADS>(r, out, 0, r.groups, whole, l.empty ? 0.0f : nan);
+        return;
+    }
+    const GradScale c = grad_scale(a.weight[row], l, lse2);
+    for (int g0 = tid;;) {
+        if (!R)
+            r.template load<U, THREADS>(g0, r.groups, q);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (g0 + u * THREADS < r.groups)
+                grad_group<DT>(r, out, g0 + u * THREADS, whole, q[u], l.inv_t, c);
+        g0 += U * THREADS;
+        if (R || g0 - tid >= r.groups)
+            break;
+    }
+    __syncthreads();  // the dense part is written
+    if (mine.id >= 0)
+        grad_list<DT>(a, l, mine, list, lse, c, out);
+}
+
+template <int DT>
+void launch_forward(int rows, const DistillArgs& a, hipStream_t s) {
+    if (rows <= 256)
+        distill_forward_kernel<DT, 1024, 4><<<dim3(rows), dim3(1024), 0, s>>>(a);
+    else
+        distill_forward_kernel<DT, 512, 4><<<dim3(rows), dim3(512), 0, s>>>(a);
+}
+
+template <int DT>
+void launch_backward(int rows, const DistillArgs& a, hipStream_t s) {
+    constexpr int kT = 256, kU = 4;
+    const long groups = static_cast<long>(a.vocab) / RowGroups<DT>::W + 2;
+    const long most = (groups + kT * kU - 1) / (kT * kU);
+    long splits = (2048 + rows - 1) / rows;
+    splits = splits < most ? splits : most;
+    distill_backward_kernel<DT, kT, kU><<<dim3(static_cast<unsigned>(rows * splits)), dim3(kT), 0, s>>>(
+        a, static_cast<int>(splits));
+}
+
+template <int DT>
+void launch_loss_grad(int rows, const DistillArgs& a, hipStream_t s) {
+    // at any alignment of the row's start
+    const long groups = (static_cast<long>(a.vocab) + RowGroups<DT>::W - 1) / RowGroups<DT>::W + 1;
+#define SPEC_RESIDENT(T, R)                                                                \
+    if (groups <= (T) * (R)) {                                                             \
+        distill_loss_grad_kernel<DT, T, R><<<dim3(rows), dim3(T), 0, s>>>(a);              \
+        return;                                                                            \
+    }
+    SPEC_RESIDENT(256, 4)
+    SPEC_RESIDENT(256, 8)
+    SPEC_RESIDENT(256, 16)
+    SPEC_RESIDENT(512, 16)
+    SPEC_RESIDENT(512, 24)
+    SPEC_RESIDENT(512, 38)
+    SPEC_RESIDENT(512, 50)
+#undef SPEC_RESIDENT
+    distill_loss_grad_kernel<DT, 1024, 0><<<dim3(rows), dim3(1024), 0, s>>>(a);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -282,7 +502,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 template <bool LOSS, bool GRAD>
 int run(int rows, int dtype, const DistillArgs& a, void* hip_stream) {
     if (rows < 0 || a.vocab < 1 || (dtype != SPEC_F32 && dtype != SPEC_BF16) || a.top_k < 1 ||
-        a.top_k > SPEC_DISTILL_MAX_K || rows >= (1L << 32) / kThreads)
+        a.top_k > SPEC_DISTILL_MAX_K || rows >= (1L << 32) / 1024)
         return SPEC_EINVAL;
     if (rows == 0)
         return SPEC_OK;
@@ -304,10 +524,13 @@ int run(int rows, int dtype, const DistillArgs& a, void* hip_stream) {
             return SPEC_EINVAL;
     }
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    if (dtype == SPEC_BF16)
-        distill_kernel<kBF16, LOSS, GRAD><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+    const bool bf16 = dtype == SPEC_BF16;
+    if (LOSS && GRAD)
+        bf16 ? launch_loss_grad<kBF16>(rows, a, s) : launch_loss_grad<kF32>(rows, a, s);
+    else if (LOSS)
+        bf16 ? launch_forward<kBF16>(rows, a, s) : launch_forward<kF32>(rows, a, s);
     else
-        distill_kernel<kF32, LOSS, GRAD><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        bf16 ? launch_backward<kBF16>(rows, a, s) : launch_backward<kF32>(rows, a, s);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
