@@ -11,9 +11,9 @@
 //     while its K largest keys are found, so the logits are read once;
 //   beam_merge: one workgroup per sequence; forms the binary64 values of the
 //     pieces' keys and keeps the K best over the beams.
-// Both narrow by a bar from their threads' largest entries (at least K entries
-// reach it, and few more do), collect what reaches it in LDS, and rank the
-// collected entries by counting. Collected in any order, ranked by a total
+// Both narrow by a bar that at least K entries reach and few more do (from the
+// threads' largest entries, and from a histogram of the values), collect what
+// reaches it in LDS, and rank the collected entries by counting. Collected in any order, ranked by a total
 // order: the result does not depend on timing.
 #include <hip/hip_runtime.h>
 
@@ -45,13 +45,6 @@ __device__ inline uint32_t ordered32(float z) {
 }
 __device__ inline float unordered32(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-__device__ inline uint64_t ordered64(double x) {
-    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x));
-    return b ^ (b >> 63 ? ~0ull : 1ull << 63);
-}
-__device__ inline double unordered64(uint64_t o) {
-    return __longlong_as_double(static_cast<long long>(o >> 63 ? o ^ (1ull << 63) : ~o));
 }
 
 // Key of a candidate; 0 marks no candidate (a finite z never has it).
@@ -274,9 +267,12 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
         const int n = count;
         const int held_keys = n < kCollect ? n : kCollect;
         const uint64_t mine = tid < held_keys ? list[tid] : 0;
-        int place = 0;
-        for (int i = 0; i < held_keys; ++i)
-            place += list[i] > mine;
+        int place = kCollect;
+        if ((tid & ~63) < held_keys) {  // wavefronts without an entry have nothing to rank
+            place = 0;
+            for (int i = 0; i < held_keys; ++i)
+                place += list[i] > mine;
+        }
         if (n <= kCollect) {
             if (tid < n) {
                 if (place < keep)
@@ -286,7 +282,7 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
             }
             return;
         }
-        if (place == keep - 1)
+        if (tid < held_keys && place == keep - 1)
             lds64[0] = mine;
         __syncthreads();
         bar_key = lds64[0];
@@ -298,9 +294,9 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
 }
 
 // A candidate of the merge in its total order: value, then the lower beam, then
-// the larger key (larger logit, lower token). value 0: none.
+// the larger key (larger logit, lower token).
 struct Cand {
-    uint64_t value;
+    double value;
     uint64_t key;
     int beam;
 };
@@ -313,126 +309,193 @@ __device__ inline bool before(const Cand& a, const Cand& b) {
     return a.key > b.key;
 }
 
+constexpr int kMergeThreads = 512;
+constexpr int kMergeWaves = kMergeThreads / 64;
+// The merge's bar: entries are counted in bins of 1/32 below the best value, and
+// all entries of the bins up to the one that holds the keep-th are collected.
+// The last bin holds everything 16 or more below.
+constexpr float kBinsPerUnit = 32.0f;
+constexpr int kEntryChunk = 8;  // keys a thread has in flight
+
 template <bool NORM>
-__global__ __launch_bounds__(kBlock) void beam_merge_kernel(
+__global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const float* __restrict__ score, const double* __restrict__ lse, int beams, int keep,
     int pieces, const uint64_t* __restrict__ keys, const NormPart* __restrict__ norm,
     int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
     __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
     __shared__ int alive[SPEC_BEAM_MAX], live[SPEC_BEAM_MAX], live_count;
-    __shared__ uint64_t bars[kBlock + 1];
+    __shared__ int hist[kMergeThreads], wave_total[kMergeWaves], limit;
+    __shared__ double wave_best[kMergeWaves];
     __shared__ Cand list[kCollect];
     __shared__ Cand next_bar;
     __shared__ int count;
     const long b = blockIdx.x;
-    const int tid = threadIdx.x;
-    if (tid == 0)
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const double none = -static_cast<double>(__builtin_huge_valf());
+    if (tid == 0) {
         count = 0;
-    for (int w = tid; w < beams; w += kBlock) {
-        const long row = b * beams + w;
-        const float sc = score[row];
-        bool ok = is_finite_f32(sc);
-        double l = 0.0;
-        if constexpr (NORM) {
-            if (ok) {
-                // log sum over the pieces, against the largest piece maximum
-                const NormPart* part = norm + row * pieces;
-                float m = -__builtin_huge_valf();
-                for (int p = 0; p < pieces; ++p)
-                    m = fmaxf(m, part[p].m);
-                double s = 0.0;
-                for (int p = 0; p < pieces; ++p) {
-                    const NormPart x = part[p];
-                    // a piece without a finite logit has sum 0, or NaN or inf
-                    s += x.m == -__builtin_huge_valf()
-                             ? x.s
-                             : x.s * exp(static_cast<double>(x.m) - static_cast<double>(m));
-                }
-                l = static_cast<double>(m) + log(s);
+        limit = kMergeThreads - 1;
+    }
+    hist[tid] = 0;
+    if constexpr (NORM) {
+        // 16 lanes to a beam: log sum over its pieces, against the largest
+        // piece maximum (a piece without a finite logit has sum 0, NaN or inf)
+        for (int w = tid >> 4; w < beams; w += kMergeThreads / 16) {
+            const long row = b * beams + w;
+            const float sc = score[row];
+            const bool ok = is_finite_f32(sc);  // else the pieces were not formed
+            const NormPart* part = norm + row * pieces;
+            float m = -__builtin_huge_valf();
+            for (int p = tid & 15; ok && p < pieces; p += 16)
+                m = fmaxf(m, part[p].m);
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1)
+                m = fmaxf(m, __shfl_xor(m, off, 64));
+            double s = 0.0;
+            for (int p = tid & 15; ok && p < pieces; p += 16) {
+                const NormPart x = part[p];
+                s += x.m == -__builtin_huge_valf()
+                         ? x.s
+                         : x.s * exp(static_cast<double>(x.m) - static_cast<double>(m));
             }
-        } else {
-            l = lse[row];
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1)
+                s += __shfl_xor(s, off, 64);
+            if ((tid & 15) == 0) {
+                const double l = static_cast<double>(m) + log(s);
+                b_score[w] = static_cast<double>(sc);
+                b_lse[w] = l;
+                alive[w] = ok && is_finite_f64(l);
+            }
         }
-        ok = ok && is_finite_f64(l);
-        b_score[w] = static_cast<double>(sc);
-        b_lse[w] = l;
-        alive[w] = ok;
+    } else if (tid < beams) {
+        const float sc = score[b * beams + tid];
+        const double l = lse[b * beams + tid];
+        b_score[tid] = static_cast<double>(sc);
+        b_lse[tid] = l;
+        alive[tid] = is_finite_f32(sc) && is_finite_f64(l);
     }
     __syncthreads();
-    if (tid < 64) {  // the live beams, in order (at most 64)
-        const bool on = tid < beams && alive[tid];
+    if (wid == 0) {  // the live beams, in order (at most 64)
+        const bool on = lane < beams && alive[lane];
         const unsigned long long mask = __ballot(on);
         if (on)
-            live[__popcll(mask & ((1ull << tid) - 1))] = tid;
-        if (tid == 0)
+            live[__popcll(mask & ((1ull << lane) - 1))] = lane;
+        if (lane == 0)
             live_count = __popcll(mask);
     }
     __syncthreads();
-    // The live beams' lists, one per piece, sorted: `share` threads to a list,
-    // thread (l, r) taking its entries r, r + share, ... The first of them is the
-    // thread's largest.
-    const int n_live = live_count;
-    const int lists = n_live * pieces;
-    const int share = lists < kBlock ? kBlock / (lists > 0 ? lists : 1) : 1;
-    const int step = kBlock / share;  // lists taken at a time
-    const uint64_t* k_b = keys + b * beams * pieces * keep;
-    auto candidate = [&](int l, int r) {
-        const int w = live[l / pieces];
-        const uint64_t key = k_b[(static_cast<long>(w) * pieces + l % pieces) * keep + r];
-        Cand x{0, key, w};
-        if (key != 0)
-            x.value = ordered64(b_score[w] + (static_cast<double>(key_logit(key)) - b_lse[w]));
-        return x;
+
+    const int per_beam = pieces * keep, total = live_count * per_beam;
+    const uint64_t* k_b = keys + b * beams * per_beam;
+    auto value_of = [&](uint64_t key, int w) {
+        return b_score[w] + (static_cast<double>(key_logit(key)) - b_lse[w]);
     };
-    const int l0 = tid / share, r0 = tid % share;
-    uint64_t best = 0;
-    if (r0 < keep && l0 < step)
-        for (int l = l0; l < lists; l += step) {
-            const uint64_t v = candidate(l, r0).value;
-            best = v > best ? v : best;
+    // The best value: the pieces' lists are sorted, so among their first entries.
+    double best = none;
+    for (int l = tid; l < live_count * pieces; l += kMergeThreads) {
+        const int w = live[l / pieces];
+        const uint64_t key = k_b[w * per_beam + l % pieces * keep];
+        if (key != 0)
+            best = fmax(best, value_of(key, w));
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        best = fmax(best, __shfl_xor(best, off, 64));
+    if (lane == 0)
+        wave_best[wid] = best;
+    __syncthreads();
+    best = wave_best[0];
+#pragma unroll
+    for (int w = 1; w < kMergeWaves; ++w)
+        best = fmax(best, wave_best[w]);
+
+    // Every entry of the live beams' lists, kEntryChunk of a thread's loads at a time.
+    auto for_each = [&](auto&& f) {
+        for (int c0 = tid; c0 < total; c0 += kEntryChunk * kMergeThreads) {
+            uint64_t key[kEntryChunk];
+            int beam[kEntryChunk];
+#pragma unroll
+            for (int i = 0; i < kEntryChunk; ++i) {
+                const int c = c0 + i * kMergeThreads;
+                const int at = c < total ? c : c0;
+                const int n = at / per_beam;
+                beam[i] = live[n];
+                key[i] = k_b[beam[i] * per_beam + at - n * per_beam];
+                if (c >= total)
+                    key[i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kEntryChunk; ++i)
+                if (key[i] != 0)
+                    f(Cand{value_of(key[i], beam[i]), key[i], beam[i]});
         }
-    const uint64_t first_bar = keep <= 32 ? kth_of_groups<4>(best, keep, bars) : kth_of_threads(best, keep, bars);
-    Cand bar{first_bar, 0, SPEC_BEAM_MAX};  // behind every candidate of that value
-    auto emit = [&](int j, const Cand& x) {
+    };
+    auto bin_of = [&](double v) {
+        return static_cast<int>(fminf(static_cast<float>(best - v) * kBinsPerUnit,
+                                      static_cast<float>(kMergeThreads - 1)));
+    };
+    for_each([&](const Cand& x) { atomicAdd(&hist[bin_of(x.value)], 1); });
+    __syncthreads();
+    {
+        int upto = hist[tid];
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(upto, off, 64);
+            upto += lane >= off ? o : 0;
+        }
+        if (lane == 63)
+            wave_total[wid] = upto;
+        __syncthreads();
+        for (int w = 0; w < wid; ++w)
+            upto += wave_total[w];
+        if (upto >= keep && upto - hist[tid] < keep)
+            limit = tid;
+        __syncthreads();
+    }
+    const int last_bin = limit;
+    auto emit = [&](int j, const Cand& x, bool some) {
         const long at = b * keep + j;
-        const bool some = x.value != 0;
         out_parent[at] = some ? x.beam : -1;
         out_token[at] = some ? key_token(x.key) : -1;
-        out_score[at] = some ? static_cast<float>(unordered64(x.value)) : -__builtin_huge_valf();
+        out_score[at] = some ? static_cast<float>(x.value) : -__builtin_huge_valf();
         if (out_logq)
             out_logq[at] = some ? static_cast<float>(static_cast<double>(key_logit(x.key)) - b_lse[x.beam])
                                 : -__builtin_huge_valf();
     };
+    Cand bar{none, 0, SPEC_BEAM_MAX};  // behind every candidate
     for (;;) {
-        if (r0 < keep && l0 < step && best != 0 && best >= bar.value) {
-            for (int l = l0; l < lists; l += step)
-                for (int r = r0; r < keep; r += share) {
-                    const Cand x = candidate(l, r);
-                    if (x.value == 0 || before(bar, x))
-                        break;  // sorted: nothing further of this list
-                    const int slot = atomicAdd(&count, 1);
-                    if (slot < kCollect)
-                        list[slot] = x;
-                }
-        }
+        for_each([&](const Cand& x) {
+            if (bin_of(x.value) > last_bin || before(bar, x))
+                return;
+            const int slot = atomicAdd(&count, 1);
+            if (slot < kCollect)
+                list[slot] = x;
+        });
         __syncthreads();
         const int n = count;
         const int held = n < kCollect ? n : kCollect;
-        const Cand mine = tid < held ? list[tid] : Cand{0, 0, SPEC_BEAM_MAX};
-        int place = 0;
-        for (int i = 0; i < held; ++i)
-            place += before(list[i], mine);
+        Cand mine{none, 0, SPEC_BEAM_MAX};
+        int place = kCollect;
+        if (tid - lane < held) {
+            if (tid < held)
+                mine = list[tid];
+            place = 0;
+            for (int i = 0; i < held; ++i)
+                place += before(list[i], mine);
+        }
         if (n <= kCollect) {
             if (tid < n) {
                 if (place < keep)
-                    emit(place, mine);
+                    emit(place, mine, true);
             } else if (tid < keep) {
-                emit(tid, Cand{0, 0, 0});
+                emit(tid, mine, false);
             }
             return;
         }
-        // Overflow: the keep-th best of those that fit is a higher bar.
-        if (place == keep - 1)
+        // Overflow (ties, or a crowded bin): the keep-th best of those that fit
+        // is a higher bar, and no two candidates are equal in the order.
+        if (tid < held && place == keep - 1)
             next_bar = mine;
         __syncthreads();
         bar = next_bar;
@@ -543,7 +606,7 @@ int spec_beam_init(int batch, int beams, int keep, int vocab, int dtype, void* h
     const long groups = (static_cast<long>(vocab) + W - 1) / W + 1;
     const long pieces = (groups + kPieceUnroll * kBlock - 1) / (kPieceUnroll * kBlock);
     const long rows = static_cast<long>(batch) * beams;
-    if (rows * pieces >= (1L << 32) / kBlock || static_cast<long>(beams) * pieces * keep >= (1L << 31))
+    if (rows * pieces >= (1L << 32) / kBlock || static_cast<long>(beams) * pieces * keep >= (1L << 30))
         return SPEC_EINVAL;
     spec_beam_ctx* ctx = new (std::nothrow) spec_beam_ctx();
     if (!ctx)
@@ -607,11 +670,11 @@ int spec_beam_select(spec_beam_ctx* ctx, const void* logits, const float* score,
         return SPEC_EHIP;
     const dim3 seqs(static_cast<unsigned>(ctx->B));
     if (lse)
-        beam_merge_kernel<false><<<seqs, dim3(kBlock), 0, s>>>(
+        beam_merge_kernel<false><<<seqs, dim3(kMergeThreads), 0, s>>>(
             score, lse, ctx->W, ctx->K, ctx->pieces, ctx->keys, ctx->norm, out_parent, out_token,
             out_score, out_logq);
     else
-        beam_merge_kernel<true><<<seqs, dim3(kBlock), 0, s>>>(
+        beam_merge_kernel<true><<<seqs, dim3(kMergeThreads), 0, s>>>(
             score, lse, ctx->W, ctx->K, ctx->pieces, ctx->keys, ctx->norm, out_parent, out_token,
             out_score, out_logq);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
