@@ -26,8 +26,12 @@
 namespace specv {
 namespace {
 
-constexpr int kPieceUnroll = 8;          // 16-byte groups of a piece per thread
-constexpr int kCollect = kBlock;         // collected entries: one per thread when ranked
+constexpr int kPieceUnroll = 8;  // 16-byte groups of a piece per thread
+constexpr int kCollect = 256;    // collected entries: one per thread when ranked
+// Threads of a piece's workgroup. What a piece costs beside its loads is
+// collecting and ranking a little more than K entries: long lists take longer
+// pieces (K = 32 at V = 128256: PIECE_FIGURES).
+constexpr int piece_threads(int keep) { return keep <= 16 ? 256 : 512; }
 // log2(e) minus its binary32 rounding: the exponent's second term keeps the
 // normaliser's error at the rounding of single exponentials instead of 1.3e-8
 // times the distance from the row's maximum.
@@ -69,50 +73,48 @@ __device__ inline T wave_sort(T v) {
     return v;
 }
 
-// The keep-th largest of the maxima of the workgroup's runs of G lanes (kBlock
-// / G of them, at most 64): every wavefront ranks all of them by counting, so
-// one barrier does. lds: kBlock / G values.
-template <int G, typename T>
-__device__ inline T kth_of_groups(T v, int keep, T* lds) {
-    constexpr int N = kBlock / G;
-    static_assert(N <= 64, "one maximum per lane");
+// The keep-th largest of the maxima of the workgroup's runs of G lanes (T / G of
+// them, at most 64), the same in every thread: a value belongs to the keep
+// largest when fewer than keep others are larger, and the smallest such value is
+// asked for. Every wavefront counts for itself, so one barrier does. lds: T / G values.
+template <int T, int G>
+__device__ inline float kth_of_groups(float v, int keep, float* lds) {
+    constexpr int N = T / G;
+    static_assert(N <= 64 && 64 % N == 0, "one maximum per lane");
 #pragma unroll
-    for (int off = 1; off < G; off <<= 1) {
-        const T o = __shfl_xor(v, off, 64);
-        v = o > v ? o : v;
-    }
+    for (int off = 1; off < G; off <<= 1)
+        v = fmaxf(v, __shfl_xor(v, off, 64));
     if (threadIdx.x % G == 0)
         lds[threadIdx.x / G] = v;
     __syncthreads();
-    const int i = (threadIdx.x & 63) % N;
-    v = lds[i];
-    int place = 0;
+    v = lds[threadIdx.x % N];
+    int larger = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const T o = lds[j];
-        place += o > v || (o == v && j < i);
-    }
-    const unsigned long long at = __ballot(place == keep - 1);
-    const int src = __ffsll(static_cast<long long>(at)) - 1;
-    return __shfl(v, src, 64);
+    for (int j = 0; j < N; ++j)
+        larger += lds[j] > v;
+    v = larger < keep ? v : __builtin_huge_valf();
+#pragma unroll
+    for (int off = 1; off < N; off <<= 1)
+        v = fminf(v, __shfl_xor(v, off, 64));
+    return v;
 }
 
 // The keep-th largest of the threads' own values: every wavefront sorts its 64;
 // a thread's place in the whole is its place in its own list plus the entries
-// before it in the others (equal values are placed by wavefront). lds: kBlock
-// values and one more.
-template <typename T>
-__device__ inline T kth_of_threads(T v, int keep, T* lds) {
+// before it in the others (equal values are placed by wavefront). lds: T values
+// and one more.
+template <int T>
+__device__ inline float kth_of_threads(float v, int keep, float* lds) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     v = wave_sort(v);
     lds[wid * 64 + lane] = v;
     __syncthreads();
     int place = lane;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < T / 64; ++w) {
         if (w == wid)
             continue;
-        const T* list = lds + w * 64;
+        const float* list = lds + w * 64;
         int lo = 0;  // entries of the list before v
 #pragma unroll
         for (int step = 64; step > 0; step >>= 1) {
@@ -123,24 +125,24 @@ __device__ inline T kth_of_threads(T v, int keep, T* lds) {
         place += lo;
     }
     if (place == keep - 1)
-        lds[kBlock] = v;
+        lds[T] = v;
     __syncthreads();
-    return lds[kBlock];
+    return lds[T];
 }
 
 // A bar that at least `keep` of the workgroup's entries reach (each thread
-// giving the largest of its own, `busy` threads having any), and few more: the
-// keep-th largest of 16 maxima over 16 threads lets about 1.4 keep (keep = 8)
-// to 3.4 keep (16) entries of evenly spread data through, of 64 maxima over
-// 4 threads 1.4 keep (32), of the threads' own 1.15 keep (64). The first
-// two cost a few lane exchanges and one barrier, the last a sort.
-template <typename T>
-__device__ inline T bar_of(T v, int keep, int busy, T* lds) {
-    if (keep <= 16 && busy >= 16 * keep)
-        return kth_of_groups<16>(v, keep, lds);
-    if (keep <= 32 && busy >= 4 * keep)
-        return kth_of_groups<4>(v, keep, lds);
-    return kth_of_threads(v, keep, lds);
+// giving the largest of its own, `busy` threads having any), and few more: of
+// evenly spread data the keep-th largest of 16 maxima lets about 1.4 keep (keep
+// = 8) to 3.4 keep (16) entries through, of 64 maxima 1.4 keep (32), of the
+// threads' own 1.15 keep (64 of 256). The maxima cost a few lane exchanges and
+// one barrier, the threads' own a sort.
+template <int T>
+__device__ inline float bar_of(float v, int keep, int busy, float* lds) {
+    if (keep <= 16 && busy >= T / 16 * keep)
+        return kth_of_groups<T, T / 16>(v, keep, lds);
+    if (keep <= 48 && busy >= T / 64 * keep)
+        return kth_of_groups<T, T / 64>(v, keep, lds);
+    return kth_of_threads<T>(v, keep, lds);
 }
 
 // Names the piece's registers, so that what was unpacked from them before is
@@ -154,8 +156,8 @@ __device__ __forceinline__ void repack(uint4 (&q)[U]) {
 
 // The K largest keys of piece p of row `row`, largest first, 0 where the piece
 // has fewer candidates; with NORM also the piece's part of the normaliser.
-template <int DT, int U, bool NORM>
-__global__ __launch_bounds__(kBlock) void beam_piece_kernel(
+template <int DT, int T, int U, bool NORM>
+__global__ __launch_bounds__(T) void beam_piece_kernel(
     const void* __restrict__ logits, const float* __restrict__ score,
     const double* __restrict__ lse, int vocab, int keep, int pieces, uint64_t* __restrict__ keys,
     NormPart* __restrict__ norm) {
@@ -176,12 +178,13 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
     const int g0 = static_cast<int>(static_cast<long>(r.groups) * p / pieces);
     const int g1 = static_cast<int>(static_cast<long>(r.groups) * (p + 1) / pieces);
     uint4 q[U];
-    r.template load<U, kBlock>(g0 + tid, g1, q);
+    r.template load<U, T>(g0 + tid, g1, q);
 
-    __shared__ float bars[kBlock + 1];
+    __shared__ float bars[T + 1];
     __shared__ uint64_t list[kCollect];
-    __shared__ uint64_t lds64[kWaves];
-    __shared__ float lds_f[kWaves];
+    __shared__ double wave_sums[T / 64];
+    __shared__ float wave_most[T / 64];
+    __shared__ uint64_t next_bar;
     __shared__ int count;
     if (tid == 0)
         count = 0;
@@ -212,11 +215,17 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
         }
     }
     const int held = g1 - g0;
-    const float bar = bar_of(best, keep, held < kBlock ? held : kBlock, bars);
+    const float bar = bar_of<T>(best, keep, held < T ? held : T, bars);
 
     repack(q);
     if constexpr (NORM) {
-        const float m = block_max(best, lds_f);
+        float m = wave_max(best);
+        if ((tid & 63) == 0)
+            wave_most[tid >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < T / 64; ++w)
+            m = fmaxf(m, wave_most[w]);
         const float ref = m == -inf ? 0.0f : m;
         double s = 0.0;
 #pragma unroll
@@ -231,35 +240,49 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
             }
             s += static_cast<double>(g);
         }
-        s = block_sum(s, reinterpret_cast<double*>(lds64));
-        if (tid == 0)
+        s = wave_sum(s);
+        if ((tid & 63) == 0)
+            wave_sums[tid >> 6] = s;
+        __syncthreads();
+        if (tid == 0) {
+            s = wave_sums[0];
+#pragma unroll
+            for (int w = 1; w < T / 64; ++w)
+                s += wave_sums[w];
             norm[row * pieces + p] = NormPart{m, 0, s};
+        }
     }
 
     // Collect the entries that reach the bar. If the list overflows (ties at the
     // bar, or a vocabulary whose best entries lie together), the keep-th largest
     // key that did fit is a higher bar, and keys are unique: again with that.
-    float bar_z = bar;
+    float bar_z = fmaxf(bar, kNegMax);  // -inf is no candidate
     uint64_t bar_key = 0;
-    int v0 = static_cast<int>(r.element(g0 + tid));
+    const int v0 = static_cast<int>(r.element(g0 + tid));
     for (;;) {
         repack(q);
-        asm volatile("" : "+v"(v0));  // nor the 64 tokens over the loop
-        if (best >= bar_z && best > -inf) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!(most[u] >= bar_z))
-                    continue;
-                float z[W];
-                Row::unpack(q[u], z);
+        for (int u = 0; u < U; ++u) {
+            if (!(most[u] >= bar_z))
+                continue;
+            float z[W];
+            Row::unpack(q[u], z);
+            unsigned hits = 0;
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    const uint64_t key = make_key(z[e], v0 + u * kBlock * W + e);
-                    if (z[e] >= bar_z && is_finite_f32(z[e]) && key >= bar_key) {
-                        const int slot = atomicAdd(&count, 1);
-                        if (slot < kCollect)
-                            list[slot] = key;
-                    }
+            for (int e = 0; e < W; ++e)
+                hits |= z[e] >= bar_z ? 1u << e : 0u;
+            while (hits) {
+                const int e = __builtin_ctz(hits);
+                hits &= hits - 1;
+                float x = z[0];
+#pragma unroll
+                for (int i = 1; i < W; ++i)
+                    x = e == i ? z[i] : x;
+                const uint64_t key = make_key(x, v0 + u * T * W + e);
+                if (x < inf && key >= bar_key) {
+                    const int slot = atomicAdd(&count, 1);
+                    if (slot < kCollect)
+                        list[slot] = key;
                 }
             }
         }
@@ -283,9 +306,9 @@ __global__ __launch_bounds__(kBlock) void beam_piece_kernel(
             return;
         }
         if (tid < held_keys && place == keep - 1)
-            lds64[0] = mine;
+            next_bar = mine;
         __syncthreads();
-        bar_key = lds64[0];
+        bar_key = next_bar;
         bar_z = key_logit(bar_key);
         if (tid == 0)
             count = 0;
@@ -481,8 +504,12 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             if (tid < held)
                 mine = list[tid];
             place = 0;
-            for (int i = 0; i < held; ++i)
-                place += before(list[i], mine);
+            for (int i = 0; i < held; ++i) {
+                const double v = list[i].value;
+                place += v > mine.value;
+                if (v == mine.value)  // itself, and ties
+                    place += before(list[i], mine);
+            }
         }
         if (n <= kCollect) {
             if (tid < n) {
@@ -604,9 +631,10 @@ int spec_beam_init(int batch, int beams, int keep, int vocab, int dtype, void* h
     // and last groups may both hang over).
     const long W = dtype == SPEC_BF16 ? 8 : 4;
     const long groups = (static_cast<long>(vocab) + W - 1) / W + 1;
-    const long pieces = (groups + kPieceUnroll * kBlock - 1) / (kPieceUnroll * kBlock);
+    const long per_piece = static_cast<long>(kPieceUnroll) * piece_threads(keep);
+    const long pieces = (groups + per_piece - 1) / per_piece;
     const long rows = static_cast<long>(batch) * beams;
-    if (rows * pieces >= (1L << 32) / kBlock || static_cast<long>(beams) * pieces * keep >= (1L << 30))
+    if (rows * pieces >= (1L << 32) / piece_threads(keep) || batch >= (1L << 32) / kMergeThreads || static_cast<long>(beams) * pieces * keep >= (1L << 30))
         return SPEC_EINVAL;
     spec_beam_ctx* ctx = new (std::nothrow) spec_beam_ctx();
     if (!ctx)
@@ -651,20 +679,28 @@ int spec_beam_select(spec_beam_ctx* ctx, const void* logits, const float* score,
         return SPEC_EINVAL;
     const dim3 grid(static_cast<unsigned>(static_cast<long>(ctx->B) * ctx->W * ctx->pieces));
     hipStream_t s = ctx->stream;
-#define SPEC_PIECE(DT, NORM)                                                                   \
-    beam_piece_kernel<DT, kPieceUnroll, NORM><<<grid, dim3(kBlock), 0, s>>>(                   \
+#define SPEC_PIECE(DT, T, NORM)                                                                \
+    beam_piece_kernel<DT, T, kPieceUnroll, NORM><<<grid, dim3(T), 0, s>>>(                     \
         logits, score, lse, ctx->V, ctx->K, ctx->pieces, ctx->keys, ctx->norm)
+#define SPEC_PIECE_T(DT, NORM)             \
+    if (piece_threads(ctx->K) == 256)      \
+        SPEC_PIECE(DT, 256, NORM);         \
+    else                                   \
+        SPEC_PIECE(DT, 512, NORM)
     if (ctx->dtype == SPEC_BF16) {
-        if (lse)
-            SPEC_PIECE(kBF16, false);
-        else
-            SPEC_PIECE(kBF16, true);
+        if (lse) {
+            SPEC_PIECE_T(kBF16, false);
+        } else {
+            SPEC_PIECE_T(kBF16, true);
+        }
     } else {
-        if (lse)
-            SPEC_PIECE(kF32, false);
-        else
-            SPEC_PIECE(kF32, true);
+        if (lse) {
+            SPEC_PIECE_T(kF32, false);
+        } else {
+            SPEC_PIECE_T(kF32, true);
+        }
     }
+#undef SPEC_PIECE_T
 #undef SPEC_PIECE
     if (hipGetLastError() != hipSuccess)
         return SPEC_EHIP;
