@@ -59,14 +59,13 @@ __device__ inline float key_logit(uint64_t k) { return unordered32(static_cast<u
 __device__ inline int key_token(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
 // The wavefront's values sorted, largest first (bitonic).
-template <typename T>
-__device__ inline T wave_sort(T v) {
+__device__ inline int wave_sort(int v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int k = 2; k <= 64; k <<= 1)
 #pragma unroll
         for (int j = k >> 1; j > 0; j >>= 1) {
-            const T o = __shfl_xor(v, j, 64);
+            const int o = __shfl_xor(v, j, 64);
             const bool keep_max = ((lane & j) == 0) == ((lane & k) == 0);
             v = (o > v) == keep_max ? o : v;
         }
@@ -78,12 +77,12 @@ __device__ inline T wave_sort(T v) {
 // largest when fewer than keep others are larger, and the smallest such value is
 // asked for. Every wavefront counts for itself, so one barrier does. lds: T / G values.
 template <int T, int G>
-__device__ inline float kth_of_groups(float v, int keep, float* lds) {
+__device__ inline int kth_of_groups(int v, int keep, int* lds) {
     constexpr int N = T / G;
     static_assert(N <= 64 && 64 % N == 0, "one maximum per lane");
 #pragma unroll
     for (int off = 1; off < G; off <<= 1)
-        v = fmaxf(v, __shfl_xor(v, off, 64));
+        v = max(v, __shfl_xor(v, off, 64));
     if (threadIdx.x % G == 0)
         lds[threadIdx.x / G] = v;
     __syncthreads();
@@ -92,10 +91,10 @@ __device__ inline float kth_of_groups(float v, int keep, float* lds) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
         larger += lds[j] > v;
-    v = larger < keep ? v : __builtin_huge_valf();
+    v = larger < keep ? v : 0x7FFFFFFF;
 #pragma unroll
     for (int off = 1; off < N; off <<= 1)
-        v = fminf(v, __shfl_xor(v, off, 64));
+        v = min(v, __shfl_xor(v, off, 64));
     return v;
 }
 
@@ -104,7 +103,7 @@ __device__ inline float kth_of_groups(float v, int keep, float* lds) {
 // before it in the others (equal values are placed by wavefront). lds: T values
 // and one more.
 template <int T>
-__device__ inline float kth_of_threads(float v, int keep, float* lds) {
+__device__ inline int kth_of_threads(int v, int keep, int* lds) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     v = wave_sort(v);
     lds[wid * 64 + lane] = v;
@@ -114,7 +113,7 @@ __device__ inline float kth_of_threads(float v, int keep, float* lds) {
     for (int w = 0; w < T / 64; ++w) {
         if (w == wid)
             continue;
-        const float* list = lds + w * 64;
+        const int* list = lds + w * 64;
         int lo = 0;  // entries of the list before v
 #pragma unroll
         for (int step = 64; step > 0; step >>= 1) {
@@ -137,7 +136,7 @@ __device__ inline float kth_of_threads(float v, int keep, float* lds) {
 // threads' own 1.15 keep (64 of 256). The maxima cost a few lane exchanges and
 // one barrier, the threads' own a sort.
 template <int T>
-__device__ inline float bar_of(float v, int keep, int busy, float* lds) {
+__device__ inline int bar_of(int v, int keep, int busy, int* lds) {
     if (keep <= 16 && busy >= T / 16 * keep)
         return kth_of_groups<T, T / 16>(v, keep, lds);
     if (keep <= 48 && busy >= T / 64 * keep)
@@ -159,8 +158,8 @@ __device__ __forceinline__ void repack(uint4 (&q)[U]) {
 template <int DT, int T, int U, bool NORM>
 __global__ __launch_bounds__(T) void beam_piece_kernel(
     const void* __restrict__ logits, const float* __restrict__ score,
-    const double* __restrict__ lse, int vocab, int keep, int pieces, uint64_t* __restrict__ keys,
-    NormPart* __restrict__ norm) {
+    const double* __restrict__ lse, int vocab, int keep, int pieces, int per_piece,
+    uint64_t* __restrict__ keys, NormPart* __restrict__ norm) {
     using Row = RowGroups<DT>;
     constexpr int W = Row::W;
     const long row = blockIdx.x / static_cast<unsigned>(pieces);
@@ -175,12 +174,12 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
         return;
     }
     const Row r(row_ptr(logits, DT, row, vocab), vocab);
-    const int g0 = static_cast<int>(static_cast<long>(r.groups) * p / pieces);
-    const int g1 = static_cast<int>(static_cast<long>(r.groups) * (p + 1) / pieces);
+    const int g0 = min(p * per_piece, r.groups);
+    const int g1 = min(g0 + per_piece, r.groups);
     uint4 q[U];
-    r.template load<U, T>(g0 + tid, g1, q);
+    r.template load<U, T>(g0, tid, g1, q);
 
-    __shared__ float bars[T + 1];
+    __shared__ int bars[T + 1];
     __shared__ uint64_t list[kCollect];
     __shared__ double wave_sums[T / 64];
     __shared__ float wave_most[T / 64];
@@ -190,36 +189,34 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
         count = 0;
 
     const float inf = __builtin_huge_valf();
-    float most[U];  // the largest of each group
-    float best = -inf;
+    int most[U];  // the largest of each group, in integer order
+    int best = Row::kOrderNegInf;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float z[W];
-        Row::unpack(q[u], z);
-        most[u] = z[0];
-#pragma unroll
-        for (int e = 1; e < W; ++e)
-            most[u] = fmaxf(most[u], z[e]);
-        best = fmaxf(best, most[u]);
+        most[u] = Row::order_max(q[u]);
+        best = max(best, most[u]);
     }
-    if (best == inf) {  // an infinite logit is no candidate
-        best = -inf;
+    if (best >= Row::kOrderInf) {  // an infinite logit or a NaN is no candidate
+        best = Row::kOrderNegInf;
         repack(q);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float z[W];
             Row::unpack(q[u], z);
+            most[u] = Row::kOrderNegInf;
 #pragma unroll
             for (int e = 0; e < W; ++e)
-                best = z[e] < inf ? fmaxf(best, z[e]) : best;
+                if (is_finite_f32(z[e]))
+                    most[u] = max(most[u], Row::order_of(z[e]));
+            best = max(best, most[u]);
         }
     }
     const int held = g1 - g0;
-    const float bar = bar_of<T>(best, keep, held < T ? held : T, bars);
+    const int bar = bar_of<T>(best, keep, held < T ? held : T, bars);
 
     repack(q);
     if constexpr (NORM) {
-        float m = wave_max(best);
+        float m = wave_max(Row::from_order(best));
         if ((tid & 63) == 0)
             wave_most[tid >> 6] = m;
         __syncthreads();
@@ -256,14 +253,15 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
     // Collect the entries that reach the bar. If the list overflows (ties at the
     // bar, or a vocabulary whose best entries lie together), the keep-th largest
     // key that did fit is a higher bar, and keys are unique: again with that.
-    float bar_z = fmaxf(bar, kNegMax);  // -inf is no candidate
+    int bar_o = max(bar, Row::kOrderNegInf + 1);  // -inf is no candidate
     uint64_t bar_key = 0;
     const int v0 = static_cast<int>(r.element(g0 + tid));
     for (;;) {
         repack(q);
+        const float bar_z = Row::from_order(bar_o);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!(most[u] >= bar_z))
+            if (most[u] < bar_o)
                 continue;
             float z[W];
             Row::unpack(q[u], z);
@@ -309,7 +307,7 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
             next_bar = mine;
         __syncthreads();
         bar_key = next_bar;
-        bar_z = key_logit(bar_key);
+        bar_o = Row::order_of(key_logit(bar_key));
         if (tid == 0)
             count = 0;
         __syncthreads();
@@ -611,6 +609,7 @@ using namespace specv;
 
 struct spec_beam_ctx {
     int B = 0, W = 0, K = 0, V = 0, dtype = 0, pieces = 0;
+    int per_piece = 0;  // groups of a piece (the last has the rest)
     hipStream_t stream = nullptr;
     void* ws = nullptr;
     uint64_t* keys = nullptr;
@@ -645,6 +644,7 @@ int spec_beam_init(int batch, int beams, int keep, int vocab, int dtype, void* h
     ctx->V = vocab;
     ctx->dtype = dtype;
     ctx->pieces = static_cast<int>(pieces);
+    ctx->per_piece = static_cast<int>(per_piece);
     ctx->stream = static_cast<hipStream_t>(hip_stream);
     const size_t key_bytes = static_cast<size_t>(rows) * pieces * keep * sizeof(uint64_t);
     const size_t norm_bytes = static_cast<size_t>(rows) * pieces * sizeof(NormPart);
@@ -681,7 +681,7 @@ int spec_beam_select(spec_beam_ctx* ctx, const void* logits, const float* score,
     hipStream_t s = ctx->stream;
 #define SPEC_PIECE(DT, T, NORM)                                                                \
     beam_piece_kernel<DT, T, kPieceUnroll, NORM><<<grid, dim3(T), 0, s>>>(                     \
-        logits, score, lse, ctx->V, ctx->K, ctx->pieces, ctx->keys, ctx->norm)
+        logits, score, lse, ctx->V, ctx->K, ctx->pieces, ctx->per_piece, ctx->keys, ctx->norm)
 #define SPEC_PIECE_T(DT, NORM)             \
     if (piece_threads(ctx->K) == 256)      \
         SPEC_PIECE(DT, 256, NORM);         \

@@ -9,8 +9,8 @@
 //   distill_backward: a row's groups are split over workgroups (nothing is
 //     summed over the vocabulary);
 //   distill_loss_grad: one workgroup per row keeps the row in registers between
-//     its normaliser and its gradient, so that the logits are read once (rows
-//     that do not fit are read twice).
+//     its normaliser and its gradient, so that the logits are read once (of rows
+//     that do not fit, the rest is read twice).
 // The dense part of the gradient is written first; a barrier later the entries
 // of the list, whose students' logits were fetched before anything was
 // written, overwrite their places (so the gradient may take the logits' place,
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
     const long row = blockIdx.x;
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
     uint4 q[U];
-    r.template load<U, THREADS>(tid, r.groups, q);
+    r.template load<U, THREADS>(0, tid, r.groups, q);
     Entry mine;
     const RowList l = reduce_list<DT>(a, row, r, mine, list);
     const float nan = __builtin_nanf("");
@@ -341,14 +341,14 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
     }
     float ref = first_reference<DT>(q[0], l.inv_t);
     double s = 0.0;
-    for (int g0 = tid;;) {
+    for (int g0 = 0;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             online_add<DT>(q[u], l.inv_t, ref, s);
         g0 += U * THREADS;
-        if (g0 - tid >= r.groups)
+        if (g0 >= r.groups)
             break;
-        r.template load<U, THREADS>(g0, r.groups, q);
+        r.template load<U, THREADS>(g0, tid, r.groups, q);
     }
     const double lse = join<THREADS / 64>(ref, s, lds) / static_cast<double>(kLog2e);
     if (tid == 0) {
@@ -359,19 +359,19 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
 }
 
 template <int DT, int THREADS, int U>
-__global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a, int splits) {
+__global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a, int splits, int per_split) {
     using Row = RowGroups<DT>;
     __shared__ ListLds list;
     const int tid = threadIdx.x;
     const long row = blockIdx.x / static_cast<unsigned>(splits);
     const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(splits));
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
-    const int g0 = static_cast<int>(static_cast<long>(r.groups) * part / splits);
-    const int g1 = static_cast<int>(static_cast<long>(r.groups) * (part + 1) / splits);
+    const int g0 = min(part * per_split, r.groups);
+    const int g1 = min(g0 + per_split, r.groups);
     bool whole;
     char* out = grad_row<DT>(a, row, r, &whole);
     uint4 q[U];
-    r.template load<U, THREADS>(g0 + tid, g1, q);
+    r.template load<U, THREADS>(g0, tid, g1, q);
     Entry mine;
     const RowList l = reduce_list<DT>(a, row, r, mine, list);
     const double lse = a.lse_in[row];
@@ -380,15 +380,15 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
         return;
     }
     const GradScale c = grad_scale(a.weight[row], l, lse * static_cast<double>(kLog2e));
-    for (int g = g0 + tid;;) {
+    for (int g = g0;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (g + u * THREADS < g1)
-                grad_group<DT>(r, out, g + u * THREADS, whole, q[u], l.inv_t, c);
+            if (g + tid + u * THREADS < g1)
+                grad_group<DT>(r, out, g + tid + u * THREADS, whole, q[u], l.inv_t, c);
         g += U * THREADS;
-        if (g - tid >= g1)
+        if (g >= g1)
             break;
-        r.template load<U, THREADS>(g, g1, q);
+        r.template load<U, THREADS>(g, tid, g1, q);
     }
     __syncthreads();  // the dense part is written
     if (mine.id >= 0) {
@@ -398,12 +398,13 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
     }
 }
 
-// R > 0: the row's groups, at most R * THREADS, stay in registers. R = 0: they
-// are read again for the gradient.
-template <int DT, int THREADS, int R>
+// The row's first R * THREADS groups stay in registers; those behind them
+// (TAIL), kTailUnroll per thread at a time, are read again for the gradient.
+constexpr int kTailUnroll = 4;
+
+template <int DT, int THREADS, int R, bool TAIL>
 __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs a) {
     using Row = RowGroups<DT>;
-    constexpr int U = R ? R : 4;
     __shared__ ListLds list;
     __shared__ double lds[2 * THREADS / 64];
     const int tid = threadIdx.x;
@@ -411,8 +412,8 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
     bool whole;
     char* out = grad_row<DT>(a, row, r, &whole);
-    uint4 q[U];
-    r.template load<U, THREADS>(tid, r.groups, q);
+    uint4 q[R];
+    r.template load<R, THREADS>(0, tid, r.groups, q);
     Entry mine;
     const RowList l = reduce_list<DT>(a, row, r, mine, list);
     const float nan = __builtin_nanf("");
@@ -420,15 +421,17 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     double s = 0.0;
     if (!l.empty && !l.bad) {
         ref = first_reference<DT>(q[0], l.inv_t);
-        for (int g0 = tid;;) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                online_add<DT>(q[u], l.inv_t, ref, s);
-            g0 += U * THREADS;
-            if (R || g0 - tid >= r.groups)
-                break;
-            r.template load<U, THREADS>(g0, r.groups, q);
-        }
+        for (int u = 0; u < R; ++u)
+            online_add<DT>(q[u], l.inv_t, ref, s);
+        if constexpr (TAIL)
+            for (int g0 = R * THREADS; g0 < r.groups; g0 += kTailUnroll * THREADS) {
+                uint4 t[kTailUnroll];
+                r.template load<kTailUnroll, THREADS>(g0, tid, r.groups, t);
+#pragma unroll
+                for (int u = 0; u < kTailUnroll; ++u)
+                    online_add<DT>(t[u], l.inv_t, ref, s);
+            }
     }
     const double lse2 = join<THREADS / 64>(ref, s, lds);
     const double lse = lse2 / static_cast<double>(kLog2e);
@@ -442,17 +445,19 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
         return;
     }
     const GradScale c = grad_scale(a.weight[row], l, lse2);
-    for (int g0 = tid;;) {
-        if (!R)
-            r.template load<U, THREADS>(g0, r.groups, q);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (g0 + u * THREADS < r.groups)
-                grad_group<DT>(r, out, g0 + u * THREADS, whole, q[u], l.inv_t, c);
-        g0 += U * THREADS;
-        if (R || g0 - tid >= r.groups)
-            break;
-    }
+    for (int u = 0; u < R; ++u)
+        if (tid + u * THREADS < r.groups)
+            grad_group<DT>(r, out, tid + u * THREADS, whole, q[u], l.inv_t, c);
+    if constexpr (TAIL)
+        for (int g0 = R * THREADS; g0 < r.groups; g0 += kTailUnroll * THREADS) {
+            uint4 t[kTailUnroll];
+            r.template load<kTailUnroll, THREADS>(g0, tid, r.groups, t);
+#pragma unroll
+            for (int u = 0; u < kTailUnroll; ++u)
+                if (g0 + tid + u * THREADS < r.groups)
+                    grad_group<DT>(r, out, g0 + tid + u * THREADS, whole, t[u], l.inv_t, c);
+        }
     __syncthreads();  // the dense part is written
     if (mine.id >= 0)
         grad_list<DT>(a, l, mine, list, lse, c, out);
@@ -473,8 +478,11 @@ void launch_backward(int rows, const DistillArgs& a, hipStream_t s) {
     const long most = (groups + kT * kU - 1) / (kT * kU);
     long splits = (2048 + rows - 1) / rows;
     splits = splits < most ? splits : most;
+    // whole steps of the workgroup, so that only the last split has a partial one
+    const long per_split = (most + splits - 1) / splits * (kT * kU);
+    splits = (groups + per_split - 1) / per_split;
     distill_backward_kernel<DT, kT, kU><<<dim3(static_cast<unsigned>(rows * splits)), dim3(kT), 0, s>>>(
-        a, static_cast<int>(splits));
+        a, static_cast<int>(splits), static_cast<int>(per_split));
 }
 
 template <int DT>
@@ -483,7 +491,7 @@ void launch_loss_grad(int rows, const DistillArgs& a, hipStream_t s) {
     const long groups = (static_cast<long>(a.vocab) + RowGroups<DT>::W - 1) / RowGroups<DT>::W + 1;
 #define SPEC_RESIDENT(T, R)                                                                \
     if (groups <= (T) * (R)) {                                                             \
-        distill_loss_grad_kernel<DT, T, R><<<dim3(rows), dim3(T), 0, s>>>(a);              \
+        distill_loss_grad_kernel<DT, T, R, false><<<dim3(rows), dim3(T), 0, s>>>(a);       \
         return;                                                                            \
     }
     SPEC_RESIDENT(256, 4)
@@ -492,9 +500,8 @@ void launch_loss_grad(int rows, const DistillArgs& a, hipStream_t s) {
     SPEC_RESIDENT(512, 16)
     SPEC_RESIDENT(512, 24)
     SPEC_RESIDENT(512, 38)
-    SPEC_RESIDENT(512, 50)
 #undef SPEC_RESIDENT
-    distill_loss_grad_kernel<DT, 1024, 0><<<dim3(rows), dim3(1024), 0, s>>>(a);
+    distill_loss_grad_kernel<DT, 512, 38, true><<<dim3(rows), dim3(512), 0, s>>>(a);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

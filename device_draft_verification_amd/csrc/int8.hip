@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const void* __res
     uint32_t wild = 0;  // all exponent bits of any element set: a NaN or infinity
     // places outside the row are loaded as -inf: they are made zero here
     auto scan = [&](int g0) {
-        r.template load<N, kBlock>(g0, r.groups, q);
+        r.template load<N, kBlock>(g0 - tid, tid, r.groups, q);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int g = g0 + u * kBlock;
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const void* __res
     const float inv = 1.0f / scale;
     for (int g0 = tid; g0 - tid < r.groups; g0 += N * kBlock) {
         if (!U)
-            r.template load<N, kBlock>(g0, r.groups, q);
+            r.template load<N, kBlock>(g0 - tid, tid, r.groups, q);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int g = g0 + u * kBlock;

@@ -64,25 +64,30 @@ struct RowGroups {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 
-    // U groups g0 + u * STEP, those at or past `end` as -inf. The whole groups
-    // are all requested before any is looked at (groups outside [full0,
-    // full1) request the nearest one inside instead).
+    // U groups base + lane + u * STEP (base the same in the whole workgroup, lane
+    // in [0, STEP)), those at or past `end` as -inf. Every step's load is issued
+    // before any value is looked at: groups that are not wholly inside the row
+    // request the nearest one that is, and are put right afterwards (skipped,
+    // by a branch that the workgroup takes together, where there are none).
     template <int U, int STEP>
-    __device__ void load(int g0, int end, uint4 (&q)[U]) const {
+    __device__ void load(int base, int lane, int end, uint4 (&q)[U]) const {
         typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+        const int stop = end < full1 ? end : full1;
         if (full1 > full0) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                int g = g0 + u * STEP;
+                int g = base + lane + u * STEP;
                 g = g < full0 ? full0 : g;
                 g = g < full1 ? g : full1 - 1;
-                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base) + g);
+                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(this->base) + g);
                 q[u] = make_uint4(v.x, v.y, v.z, v.w);
             }
         }
+        if (base >= full0 && base + U * STEP <= stop)
+            return;
         // The groups at the row's ends: the first can only be this thread's
         // first, the last any one of its groups.
-        const int tail = groups - 1;
+        const int g0 = base + lane, tail = groups - 1;
         const bool has_tail = !inside(tail) && tail >= g0 && tail < end && (tail - g0) % STEP == 0 &&
                               tail - g0 < U * STEP;
         uint4 last = neg_inf();
@@ -98,6 +103,45 @@ struct RowGroups {
             else if (has_tail && g == tail)
                 q[u] = last;
         }
+    }
+
+    // The group's largest element in an integer order: for a sign-magnitude x,
+    // x ^ ((x >> all but the sign) without the sign) rises with x, two bf16 to an
+    // instruction. Unlike the floating maximum it needs no step that quiets
+    // NaNs; a positive NaN comes out above infinity, a negative one below -inf.
+    __device__ static int order_max(const uint4& q) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        if constexpr (DT == kBF16) {
+            typedef short s16x2 __attribute__((ext_vector_type(2)));
+            s16x2 m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const s16x2 x = __builtin_bit_cast(s16x2, w[i]);
+                const uint32_t sign = __builtin_bit_cast(uint32_t, x >> 15) & 0x7FFF7FFFu;
+                const s16x2 o = __builtin_bit_cast(s16x2, w[i] ^ sign);
+                m = i ? __builtin_elementwise_max(m, o) : o;
+            }
+            return m.x > m.y ? m.x : m.y;
+        } else {
+            int m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int x = static_cast<int>(w[i]);
+                const int o = x ^ ((x >> 31) & 0x7FFFFFFF);
+                m = i ? (o > m ? o : m) : o;
+            }
+            return m;
+        }
+    }
+    static constexpr int kOrderInf = DT == kBF16 ? 0x7F80 : 0x7F800000;  // of +inf
+    static constexpr int kOrderNegInf = DT == kBF16 ? -0x7F81 : static_cast<int>(0x807FFFFFu);
+    __device__ static int order_of(float z) {
+        const int x = static_cast<int>(__float_as_uint(z)) >> (DT == kBF16 ? 16 : 0);
+        return x ^ ((x >> 31) & (DT == kBF16 ? 0x7FFF : 0x7FFFFFFF));
+    }
+    __device__ static float from_order(int o) {
+        const int x = o ^ ((o >> 31) & (DT == kBF16 ? 0x7FFF : 0x7FFFFFFF));
+        return __uint_as_float(static_cast<uint32_t>(x) << (DT == kBF16 ? 16 : 0));
     }
 
     __device__ static void unpack(const uint4& q, float (&z)[W]) {

@@ -73,8 +73,8 @@ int spec_distill_backward(int rows, int vocab, int dtype, int top_k, const void*
                           void* out_grad, void* hip_stream);
 
 /* Both at once, where the weights are known before the loss is: the logits
- * are read once instead of twice (rows up to the size that one workgroup
- * holds on chip; longer ones are read again). */
+ * are read once instead of twice (the first 311 296 bytes of a row, which one
+ * workgroup keeps in registers; what is behind them is read again). */
 int spec_distill_loss_grad(int rows, int vocab, int dtype, int top_k, const void* logits,
                            const int32_t* ids, const float* teacher, const double* teacher_lse,
                            const float* temperature, const float* weight, float* out_loss,
