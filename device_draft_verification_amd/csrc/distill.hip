@@ -66,30 +66,59 @@ struct ListLds {
     double sum[4], inner[4];
 };
 
+// The workgroup's barrier for exchanges through LDS: unlike __syncthreads it
+// does not wait for global loads, so that a row stays on its way while its list
+// is reduced. The empty asm keeps the compiler from moving accesses across.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    // s_waitcnt: lgkmcnt 0, vmcnt and expcnt at their largest (not waited)
+    __builtin_amdgcn_s_waitcnt((0xF) | (0x3 << 14) | (0x7 << 4));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+struct ListFetch {
+    float t;      // the row's temperature
+    float y;      // the thread's teacher logit
+    double norm;  // teacher_lse, where given
+};
+
+// The thread's entry, and then (gather) the student's logit at it. Issued
+// before the row's own loads: loads return in order, so waiting for these then
+// waits for nothing else.
+__device__ __forceinline__ ListFetch fetch_list(const DistillArgs& a, long row, Entry& mine) {
+    const int tid = threadIdx.x;
+    ListFetch f{a.temperature[row], 0.0f, a.teacher_lse ? a.teacher_lse[row] : 0.0};
+    mine = Entry{-1, 0.0f, 0.0};
+    if (tid < a.top_k) {
+        mine.id = a.ids[row * a.top_k + tid];
+        f.y = a.teacher[row * a.top_k + tid];
+    }
+    return f;
+}
+
+template <int DT>
+__device__ __forceinline__ void gather(const DistillArgs& a, const RowGroups<DT>& r, Entry& mine) {
+    if (mine.id >= 0 && mine.id < a.vocab)
+        mine.x = r.at(mine.id);
+}
+
 // With e_j = exp(y_j - m): over the list (teacher_lse NULL, m its largest y)
 // p_j = e_j / S and log p_j = y_j - m - log S, S = sum e; so sum p (log p - x)
 // = T / S - log S with T = sum e (y - m - x): S and T in one exchange. With
 // the teacher's own normaliser as m, p = e, P = S and the sum is T.
-template <int DT>
-__device__ inline RowList reduce_list(const DistillArgs& a, long row, const RowGroups<DT>& r,
-                                      Entry& mine, ListLds& lds) {
+__device__ inline RowList reduce_list(const DistillArgs& a, const ListFetch& f, Entry& mine, ListLds& lds) {
     const int tid = threadIdx.x, wid = tid >> 6;
     const float inf = __builtin_huge_valf();
     RowList out{};
-    const bool t_ok = temperature_mode(a.temperature[row], &out.inv_t) == 1;
-    mine = Entry{-1, 0.0f, 0.0};
-    float y = -inf;
-    if (tid < a.top_k) {
-        const int id = a.ids[row * a.top_k + tid];
-        if (id >= 0) {
-            mine.id = id;
-            y = a.teacher[row * a.top_k + tid] * out.inv_t;
-            if (id < a.vocab)
-                mine.x = r.at(id) * out.inv_t;
-        }
-    }
+    const bool t_ok = temperature_mode(f.t, &out.inv_t) == 1;
+    const bool used = mine.id >= 0;
+    const float y = used ? f.y * out.inv_t : -inf;
+    // The student's logit has to be here before anybody writes the gradient,
+    // which may take the logits' place.
+    asm volatile("" : "+v"(mine.x));
+    mine.x *= out.inv_t;
     if (tid < SPEC_DISTILL_MAX_K) {
-        const bool used = mine.id >= 0;
         const bool any_used = __ballot(used) != 0, any_out = __ballot(used && mine.id >= a.vocab) != 0,
                    any_mass = __ballot(used && !(y == -inf)) != 0;
         const float m = wave_max(y);
@@ -98,18 +127,18 @@ __device__ inline RowList reduce_list(const DistillArgs& a, long row, const RowG
             lds.flags[wid] = (any_used ? 1 : 0) | (any_out ? 2 : 0) | (any_mass ? 4 : 0);
         }
     }
-    __syncthreads();
+    lds_barrier();
     const int flags = lds.flags[0] | lds.flags[1] | lds.flags[2] | lds.flags[3];
     const bool own_norm = a.teacher_lse != nullptr;
     out.bad = !t_ok || (flags & 2);
     out.empty = !(flags & 1) || (!out.bad && !own_norm && !(flags & 4));
-    const double m = own_norm ? a.teacher_lse[row]
+    const double m = own_norm ? f.norm
                               : static_cast<double>(fmaxf(fmaxf(lds.most[0], lds.most[1]),
                                                           fmaxf(lds.most[2], lds.most[3])));
     double e = 0.0;
     if (tid < SPEC_DISTILL_MAX_K) {
         double t = 0.0;
-        if (mine.id >= 0) {
+        if (used) {
             const double d = static_cast<double>(y) - m;
             e = exp(d);
             if (!(e == 0.0))
@@ -121,7 +150,7 @@ __device__ inline RowList reduce_list(const DistillArgs& a, long row, const RowG
             lds.inner[wid] = w;
         }
     }
-    __syncthreads();
+    lds_barrier();
     const double s = (lds.sum[0] + lds.sum[1]) + (lds.sum[2] + lds.sum[3]);
     const double t = (lds.inner[0] + lds.inner[1]) + (lds.inner[2] + lds.inner[3]);
     out.bad = out.bad || !is_finite_f64(m) || !is_finite_f64(s);
@@ -199,7 +228,7 @@ __device__ inline double join(float ref, double s, double* lds) {
         lds[2 * (threadIdx.x >> 6)] = static_cast<double>(m);
         lds[2 * (threadIdx.x >> 6) + 1] = s;
     }
-    __syncthreads();
+    lds_barrier();
     double top = lds[0];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w)
@@ -225,6 +254,25 @@ __device__ inline void store_element(void* row, long v, float g) {
     }
 }
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ u32x4 pack_group(const float (&d)[RowGroups<DT>::W]) {
+    u32x4 v;
+    if constexpr (DT == kBF16) {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{d[2 * i], d[2 * i + 1]}, bf16x2));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __float_as_uint(d[i]);
+    }
+    return v;
+}
+
 // Group g of the row's gradient; `whole`: it can go out as one 16-byte store.
 template <int DT>
 __device__ inline void store_group(const RowGroups<DT>& r, char* out, int g, bool whole,
@@ -232,20 +280,7 @@ __device__ inline void store_group(const RowGroups<DT>& r, char* out, int g, boo
     constexpr int W = RowGroups<DT>::W;
     const long e0 = r.element(g);
     if (whole && r.inside(g)) {
-        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-        u32x4 v;
-        if constexpr (DT == kBF16) {
-            typedef float f32x2 __attribute__((ext_vector_type(2)));
-            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{d[2 * i], d[2 * i + 1]}, bf16x2));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = __float_as_uint(d[i]);
-        }
-        *reinterpret_cast<u32x4*>(out + e0 * RowGroups<DT>::ESZ) = v;
+        *reinterpret_cast<u32x4*>(out + e0 * RowGroups<DT>::ESZ) = pack_group<DT>(d);
         return;
     }
 #pragma unroll
@@ -279,6 +314,19 @@ __device__ __forceinline__ void grad_group(const RowGroups<DT>& r, char* out, in
     for (int e = 0; e < W; ++e)
         d[e] = c.dense * fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -c.ref));
     store_group<DT>(r, out, g, whole, d);
+}
+
+// A group wholly inside a row whose gradient has the row's alignment.
+template <int DT>
+__device__ __forceinline__ void grad_group_inside(const RowGroups<DT>& r, char* out, int g, const uint4& q,
+                                                  float inv_t, const GradScale& c) {
+    constexpr int W = RowGroups<DT>::W;
+    float z[W], d[W];
+    RowGroups<DT>::unpack(q, z);
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+        d[e] = c.dense * fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -c.ref));
+    reinterpret_cast<u32x4*>(out - r.shift * RowGroups<DT>::ESZ)[g] = pack_group<DT>(d);
 }
 
 template <int DT, int THREADS>
@@ -327,10 +375,12 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
     const int tid = threadIdx.x;
     const long row = blockIdx.x;
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
-    uint4 q[U];
-    r.template load<U, THREADS>(0, tid, r.groups, q);
     Entry mine;
-    const RowList l = reduce_list<DT>(a, row, r, mine, list);
+    const ListFetch f = fetch_list(a, row, mine);
+    gather<DT>(a, r, mine);
+    uint4 q[U];
+    r.template load<U, THREADS, true>(0, tid, r.groups, q);
+    const RowList l = reduce_list(a, f, mine, list);
     const float nan = __builtin_nanf("");
     if (l.empty || l.bad) {
         if (tid == 0) {
@@ -370,11 +420,13 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
     const int g1 = min(g0 + per_split, r.groups);
     bool whole;
     char* out = grad_row<DT>(a, row, r, &whole);
+    Entry mine;
+    const ListFetch f = fetch_list(a, row, mine);
+    const double lse = a.lse_in[row];
+    gather<DT>(a, r, mine);
     uint4 q[U];
     r.template load<U, THREADS>(g0, tid, g1, q);
-    Entry mine;
-    const RowList l = reduce_list<DT>(a, row, r, mine, list);
-    const double lse = a.lse_in[row];
+    const RowList l = reduce_list(a, f, mine, list);
     if (l.empty || l.bad || !is_finite_f64(lse)) {
         fill<DT, THREADS>(r, out, g0, g1, whole, l.empty ? 0.0f : __builtin_nanf(""));
         return;
@@ -400,6 +452,8 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
 
 // The row's first R * THREADS groups stay in registers; those behind them
 // (TAIL), kTailUnroll per thread at a time, are read again for the gradient.
+// (Workgroups that stay for several rows and load the next row's groups as the
+// gradients free their registers measured the same at N = 2304, V = 152064.)
 constexpr int kTailUnroll = 4;
 
 template <int DT, int THREADS, int R, bool TAIL>
@@ -412,10 +466,12 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
     bool whole;
     char* out = grad_row<DT>(a, row, r, &whole);
-    uint4 q[R];
-    r.template load<R, THREADS>(0, tid, r.groups, q);
     Entry mine;
-    const RowList l = reduce_list<DT>(a, row, r, mine, list);
+    const ListFetch f = fetch_list(a, row, mine);
+    gather<DT>(a, r, mine);
+    uint4 q[R];
+    r.template load<R, THREADS, true>(0, tid, r.groups, q);
+    const RowList l = reduce_list(a, f, mine, list);
     const float nan = __builtin_nanf("");
     float ref = kNegMax;
     double s = 0.0;
@@ -445,19 +501,23 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
         return;
     }
     const GradScale c = grad_scale(a.weight[row], l, lse2);
+    // Steps that lie wholly inside the row go out as 16-byte stores from
+    // registers; the others, at the row's ends (or of a gradient that is
+    // aligned otherwise than its row), are read again.
+    auto from_registers = [&](int u) {
+        return whole && u < R && u * THREADS >= r.full0 && (u + 1) * THREADS <= r.full1;
+    };
 #pragma unroll
     for (int u = 0; u < R; ++u)
-        if (tid + u * THREADS < r.groups)
-            grad_group<DT>(r, out, tid + u * THREADS, whole, q[u], l.inv_t, c);
-    if constexpr (TAIL)
-        for (int g0 = R * THREADS; g0 < r.groups; g0 += kTailUnroll * THREADS) {
-            uint4 t[kTailUnroll];
-            r.template load<kTailUnroll, THREADS>(g0, tid, r.groups, t);
-#pragma unroll
-            for (int u = 0; u < kTailUnroll; ++u)
-                if (g0 + tid + u * THREADS < r.groups)
-                    grad_group<DT>(r, out, g0 + tid + u * THREADS, whole, t[u], l.inv_t, c);
-        }
+        if (from_registers(u))
+            grad_group_inside<DT>(r, out, tid + u * THREADS, q[u], l.inv_t, c);
+    const int steps = (r.groups + THREADS - 1) / THREADS;
+#pragma unroll 1
+    for (int u = 0; u < steps; ++u) {
+        const int g = tid + u * THREADS;
+        if (!from_registers(u) && g < r.groups)
+            grad_group<DT>(r, out, g, whole, r.load_any(g, r.groups), l.inv_t, c);
+    }
     __syncthreads();  // the dense part is written
     if (mine.id >= 0)
         grad_list<DT>(a, l, mine, list, lse, c, out);

@@ -26,7 +26,9 @@ struct RowGroups {
 
     __device__ RowGroups(const void* p, int v)
         : start(static_cast<const char*>(p)),
-          base(reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15))),
+          // by an offset, not through an integer: the compiler then still knows it
+          // for global memory (a flat load also counts as an LDS access)
+          base(static_cast<const char*>(p) - (reinterpret_cast<uintptr_t>(p) & 15)),
           shift(static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / ESZ)),
           vocab(v) {
         // in 64 bits: shift + vocab may pass 2^31
@@ -69,20 +71,36 @@ struct RowGroups {
     // before any value is looked at: groups that are not wholly inside the row
     // request the nearest one that is, and are put right afterwards (skipped,
     // by a branch that the workgroup takes together, where there are none).
-    template <int U, int STEP>
+    // STEPWISE: whole steps among partial ones are left alone, too, so that
+    // their loads stay on their way.
+    template <int U, int STEP, bool STEPWISE = false>
     __device__ void load(int base, int lane, int end, uint4 (&q)[U]) const {
-        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-        const int stop = end < full1 ? end : full1;
         if (full1 > full0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                int g = base + lane + u * STEP;
-                g = g < full0 ? full0 : g;
-                g = g < full1 ? g : full1 - 1;
-                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(this->base) + g);
-                q[u] = make_uint4(v.x, v.y, v.z, v.w);
-            }
+            for (int u = 0; u < U; ++u)
+                q[u] = request(base + lane + u * STEP);
         }
+        settle<U, STEP, STEPWISE>(base, lane, end, q);
+    }
+
+    // Group g, or the nearest one that lies wholly inside the row (which has one).
+    __device__ __forceinline__ uint4 request(int g) const {
+        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+        g = g < full0 ? full0 : g;
+        g = g < full1 ? g : full1 - 1;
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base) + g);
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
+
+    __device__ uint4 load_any(int g, int end) const {
+        if (g >= end)
+            return neg_inf();
+        return inside(g) ? request(g) : load_end(g);
+    }
+
+    template <int U, int STEP, bool STEPWISE>
+    __device__ void settle(int base, int lane, int end, uint4 (&q)[U]) const {
+        const int stop = end < full1 ? end : full1;
         if (base >= full0 && base + U * STEP <= stop)
             return;
         // The groups at the row's ends: the first can only be this thread's
@@ -97,6 +115,8 @@ struct RowGroups {
             q[0] = load_end(0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (STEPWISE && base + (u + 1) * STEP <= stop)
+                continue;
             const int g = g0 + u * STEP;
             if (g >= end)
                 q[u] = neg_inf();
