@@ -25,88 +25,120 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // smallest subnormal scales overflows; those divide); for the right integer r
 // the remainder x - r * scale is a multiple of the smaller operand's last place
 // and at most half a scale in size, so the fma below is exact and decides.
-__device__ inline float exact_quotient(float x, float scale, float inv) {
+__device__ inline int exact_quotient(float x, float scale, float inv) {
     float r = __builtin_rintf(inv == __builtin_huge_valf() ? x / scale : x * inv);
     const float rem = __builtin_fmaf(-r, scale, x);
     const float twice = 2.0f * fabsf(rem);
     const bool odd = (static_cast<int>(r) & 1) != 0;
     if (twice > scale || (twice == scale && odd))
         r += rem > 0.0f ? 1.0f : -1.0f;
-    return fminf(fmaxf(r, -127.0f), 127.0f);
+    return static_cast<int>(fminf(fmaxf(r, -127.0f), 127.0f));
 }
 
-// One workgroup per row, the row in registers between its maximum and its
-// quotients (U groups per thread; U = 0: a longer row, read twice).
-template <int DT, int U>
-__global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const void* __restrict__ x, int cols,
-                                                              int8_t* __restrict__ out_q,
-                                                              float* __restrict__ out_scale) {
+// A group's quotients as bytes. Adding 1.5 * 2^23 rounds to an integer, ties to
+// even, and leaves it in the low byte; only where a remainder reaches half a
+// scale (a tie, or a product x * inv on the wrong side of one) the group takes
+// the exact way.
+template <int W>
+__device__ inline void quantize_group(const float (&x)[W], float scale, float inv, uint32_t (&b)[2]) {
+    constexpr float kMagic = 12582912.0f;
+    const float half = 0.5f * scale;
+    uint32_t w[W];
+    bool near = !(scale >= 1.17549435e-38f);  // subnormal: half a scale may not be exact
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        const float m = __builtin_amdgcn_fmed3f(x[e] * inv, -127.0f, 127.0f) + kMagic;
+        w[e] = __float_as_uint(m);
+        near = near || fabsf(__builtin_fmaf(-(m - kMagic), scale, x[e])) >= half;
+    }
+    if (near) {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            w[e] = static_cast<uint32_t>(exact_quotient(x[e], scale, inv));
+    }
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+        // v_perm_b32(a, b, s): byte k of the result is byte s[k] of {a, b}, b's first
+        const uint32_t lo = __builtin_amdgcn_perm(w[4 * i + 1], w[4 * i], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(w[4 * i + 3], w[4 * i + 2], 0x04000c0cu);
+        b[i] = lo | hi;
+    }
+}
+
+// One workgroup of T threads per row, the row in registers between its maximum
+// and its quotients (U groups per thread; LONG: a longer row, read twice).
+template <int DT, int T, int U, bool LONG>
+__global__ __launch_bounds__(T) void quantize_rows_kernel(const void* __restrict__ x, int cols,
+                                                          int8_t* __restrict__ out_q,
+                                                          float* __restrict__ out_scale) {
     using Row = RowGroups<DT>;
     constexpr int W = Row::W;
-    constexpr int N = U ? U : 4;  // groups in registers at a time
-    __shared__ float lds_f[kWaves];
+    __shared__ uint32_t lds_m[T / 64];
     const long row = blockIdx.x;
     const int tid = threadIdx.x;
     const Row r(row_ptr(x, DT, row, cols), cols);
     int8_t* q_row = out_q + row * cols;
     // a group's 8-bit values go out as one W-byte store
     const bool whole = ((reinterpret_cast<uintptr_t>(q_row) - r.shift) & (W - 1)) == 0;
-    uint4 q[N];
-    float m = 0.0f;
-    uint32_t wild = 0;  // all exponent bits of any element set: a NaN or infinity
-    // places outside the row are loaded as -inf: they are made zero here
-    auto scan = [&](int g0) {
-        r.template load<N, kBlock>(g0 - tid, tid, r.groups, q);
+    uint4 q[U];
+    // The largest magnitude as an integer: the order of floats without a sign
+    // is the order of their bits, and a NaN or infinity comes out on top.
+    uint32_t m = 0;
+    for (int g0 = 0; g0 < r.groups; g0 += U * T) {
+        r.template load<U, T>(g0, tid, r.groups, q);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int g = g0 + u * kBlock;
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + tid + u * T;
             float z[W];
             Row::unpack(q[u], z);
             if (g >= r.groups)
                 continue;
+            const bool inside = r.inside(g);
+            const long k0 = r.element(g);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const long k = r.element(g) + e;
-                const bool in = r.inside(g) || (k >= 0 && k < cols);
-                const uint32_t mag = in ? __float_as_uint(z[e]) & 0x7FFFFFFFu : 0u;
-                wild |= mag >= 0x7F800000u;
-                m = fmaxf(m, __uint_as_float(mag));
+                // places outside the row are loaded as -inf: they do not count
+                const uint32_t mag = __float_as_uint(z[e]) & 0x7FFFFFFFu;
+                if (inside || (k0 + e >= 0 && k0 + e < cols))
+                    m = mag > m ? mag : m;
             }
         }
-    };
-    for (int g0 = tid; g0 - tid < r.groups; g0 += N * kBlock) {
-        scan(g0);
-        if (U)
+        if (!LONG)
             break;
     }
-    m = wave_max(m);
-    if ((tid & 63) == 0)
-        lds_f[tid >> 6] = m;
-    const bool any_wild = __syncthreads_or(wild != 0);
-    m = fmaxf(fmaxf(lds_f[0], lds_f[1]), fmaxf(lds_f[2], lds_f[3]));
-    float scale = m / 127.0f;  // correctly rounded
-    if (any_wild)
-        scale = __builtin_nanf("");
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const uint32_t o = __shfl_xor(m, off, 64);
+        m = o > m ? o : m;
+    }
+    if constexpr (T > 64) {
+        if ((tid & 63) == 0)
+            lds_m[tid >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < T / 64; ++w) {
+            const uint32_t o = lds_m[w];
+            m = o > m ? o : m;
+        }
+    }
+    const float scale = m >= 0x7F800000u ? __builtin_nanf("") : __uint_as_float(m) / 127.0f;  // correctly rounded
     if (tid == 0)
         out_scale[row] = scale;
     const bool zero = !(scale > 0.0f);
     const float inv = 1.0f / scale;
-    for (int g0 = tid; g0 - tid < r.groups; g0 += N * kBlock) {
-        if (!U)
-            r.template load<N, kBlock>(g0 - tid, tid, r.groups, q);
+    for (int g0 = 0; g0 < r.groups; g0 += U * T) {
+        if (LONG)
+            r.template load<U, T>(g0, tid, r.groups, q);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int g = g0 + u * kBlock;
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + tid + u * T;
             if (g >= r.groups)
                 continue;
             float z[W];
             Row::unpack(q[u], z);
             uint32_t b[2] = {0, 0};
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const int v = zero ? 0 : static_cast<int>(exact_quotient(z[e], scale, inv));
-                b[e >> 2] |= (static_cast<uint32_t>(v) & 0xFFu) << (8 * (e & 3));
-            }
+            if (!zero)
+                quantize_group<W>(z, scale, inv, b);
             const long k0 = r.element(g);
             if (whole && r.inside(g)) {
                 if constexpr (W == 8)
@@ -120,7 +152,7 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const void* __res
                         q_row[k0 + e] = static_cast<int8_t>(b[e >> 2] >> (8 * (e & 3)));
             }
         }
-        if (U)
+        if (!LONG)
             break;
     }
 }
@@ -129,16 +161,23 @@ template <int DT>
 hipError_t launch_quantize(int rows, int cols, const void* x, int8_t* out_q, float* out_scale,
                            hipStream_t s) {
     constexpr int W = RowGroups<DT>::W;
-    const long groups = (static_cast<long>(cols) + W - 1) / W + 1;  // at any alignment
-    const dim3 grid(rows), block(kBlock);
-    if (groups <= kBlock)
-        quantize_rows_kernel<DT, 1><<<grid, block, 0, s>>>(x, cols, out_q, out_scale);
-    else if (groups <= 2 * kBlock + 1)
-        quantize_rows_kernel<DT, 3><<<grid, block, 0, s>>>(x, cols, out_q, out_scale);
-    else if (groups <= 8 * kBlock)
-        quantize_rows_kernel<DT, 8><<<grid, block, 0, s>>>(x, cols, out_q, out_scale);
+    const bool even = cols % W == 0 && aligned(x, 16);
+    const long groups = (static_cast<long>(cols) + W - 1) / W + (even ? 0 : 1);  // at any alignment
+#define SPEC_QUANTIZE(T, U, LONG)                                                              \
+    quantize_rows_kernel<DT, T, U, LONG><<<dim3(rows), dim3(T), 0, s>>>(x, cols, out_q, out_scale)
+    if (groups <= 128)
+        SPEC_QUANTIZE(64, 2, false);
+    else if (groups <= 256)
+        SPEC_QUANTIZE(64, 4, false);
+    else if (groups <= 512)
+        SPEC_QUANTIZE(128, 4, false);
+    else if (groups <= 1024)
+        SPEC_QUANTIZE(256, 4, false);
+    else if (groups <= 2048)
+        SPEC_QUANTIZE(256, 8, false);
     else
-        quantize_rows_kernel<DT, 0><<<grid, block, 0, s>>>(x, cols, out_q, out_scale);
+        SPEC_QUANTIZE(256, 8, true);
+#undef SPEC_QUANTIZE
     return hipGetLastError();
 }
 
@@ -152,9 +191,10 @@ hipError_t launch_quantize(int rows, int cols, const void* x, int8_t* out_q, flo
 // K in stages of 64 bytes through a ring of LDS slots, loaded straight into LDS
 // RING - 1 stages ahead: one barrier per stage, after which the slot of the
 // stage before is refilled. A slot holds TV + TN rows of 64 bytes; a row's four
-// 16-byte chunks sit at positions XORed with (row / 2) % 4, so the eight rows
-// that a phase of a fragment read touches lie in eight different 16-byte
-// places of 128.
+// 16-byte chunks sit at positions XORed with (row / 4) % 4, so the sixteen rows
+// that a phase of a fragment read touches lie in sixteen different 16-byte
+// places of the 256 bytes of the banks ((row / 2) % 4 measured one conflict
+// cycle for every useful one).
 // Rows past the end repeat the last one (their outputs are not stored), chunks
 // past the depth come from a page of zeros.
 constexpr int kStageK = 64;
@@ -192,7 +232,10 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
     constexpr int kRowBytes = 32 * MV * ESZ + 16;
     constexpr int kTurn = 32 * kRowBytes;
     constexpr int kLds = RING * kSlot > kWavesHere * kTurn ? RING * kSlot : kWavesHere * kTurn;
-    __shared__ __align__(16) int8_t lds[kLds];
+    // One LDS object: with two the compiler keeps their accesses apart by alias
+    // scopes, and then waits for every load into LDS before any read of it.
+    __shared__ __align__(16) int8_t lds[kLds + TV * sizeof(float)];
+    float* scale_v = reinterpret_cast<float*>(lds + kLds);
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     // Workgroups go round the eight XCDs: each XCD takes a contiguous run of
@@ -202,6 +245,8 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
     const int tile = xcd * per + (xcd < extra ? xcd : extra) + at;
     const int v0 = tile / tiles_n * TV;
     const int n0 = tile % tiles_n * TN;
+    for (int t = threadIdx.x; t < TV; t += 64 * WV * WN)  // read behind the loop's barriers
+        scale_v[t] = w_scale[v0 + t < cols ? v0 + t : cols - 1];
 
     // This lane's chunk of each of its wavefront's loads.
     const int8_t* src[kLoads];
@@ -209,7 +254,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int row = (wid + kWavesHere * i) * 16 + (lane >> 2);
-        chunk[i] = ((lane & 3) ^ ((row >> 1) & 3)) * 16;
+        chunk[i] = ((lane & 3) ^ ((row >> 2) & 3)) * 16;
         if (row < TV) {
             const int v = v0 + row;
             src[i] = w + static_cast<size_t>(v < cols ? v : cols - 1) * depth + chunk[i];
@@ -221,16 +266,13 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
     const int stages = (depth + kStageK - 1) / kStageK;
     const int8_t* zeros = reinterpret_cast<const int8_t*>(&zero_chunk);
     asm volatile("" : "+s"(zeros));  // looked up once, not in every stage
-    auto issue = [&](int s) {
+    auto issue = [&](int s, int i) {
         int8_t* slot = lds + (s % RING) * kSlot;
         const int k = s * kStageK;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            // stages past the end load zeros into slots that nobody reads
-            const int8_t* from = k + kStageK <= depth || k + chunk[i] < depth ? src[i] + k : zeros;
-            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from),
-                                             slot + (wid + kWavesHere * i) * 1024, 16, 0, 0);
-        }
+        // stages past the end load zeros into slots that nobody reads
+        const int8_t* from = k + kStageK <= depth || k + chunk[i] < depth ? src[i] + k : zeros;
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from),
+                                         slot + (wid + kWavesHere * i) * 1024, 16, 0, 0);
     };
     i32x16 acc[MV][MN];
 #pragma unroll
@@ -240,44 +282,65 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
             acc[i][j] = i32x16{};
 #pragma unroll
     for (int s = 0; s < RING - 1; ++s)
-        issue(s);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            issue(s, i);
     const int wv = wid % WV * (TV / WV), wn = wid / WV * (TN / WN);
     const int frag_row = lane & 31;
-    const int swz = (frag_row >> 1) & 3;  // rows of a tile start at multiples of 32
+    const int swz = (frag_row >> 2) & 3;  // rows of a tile start at multiples of 32
     // Half a stage (32 of K) is multiplied while the next half's fragments are
     // read: of stage s - 1 the second half waits in registers over the barrier.
+    // The fragment reads and loads go between the matrix instructions, in whose
+    // shadow they issue: in one run before them, all wavefronts issue theirs
+    // together behind the barrier with the matrix cores idle (1486 us against
+    // 1380 at N = 2304, D = 4096, V = 152064).
+    constexpr int kReads = MV + MN, kMul = MV * MN;
     i32x4 fw[2][MV], fa[2][MN];
-    auto read = [&](int s, int half) {
+    auto read = [&](int s, int half, int i) {
         const int8_t* slot = lds + (s % RING) * kSlot;
         const int pos = ((2 * half + (lane >> 5)) ^ swz) * 16;
-#pragma unroll
-        for (int j = 0; j < MN; ++j)
-            fa[half][j] = *reinterpret_cast<const i32x4*>(slot + (TV + wn + 32 * j + frag_row) * kStageK + pos);
-#pragma unroll
-        for (int i = 0; i < MV; ++i)
-            fw[half][i] = *reinterpret_cast<const i32x4*>(slot + (wv + 32 * i + frag_row) * kStageK + pos);
+        if (i < MN)
+            fa[half][i] = *reinterpret_cast<const i32x4*>(slot + (TV + wn + 32 * i + frag_row) * kStageK + pos);
+        else
+            fw[half][i - MN] =
+                *reinterpret_cast<const i32x4*>(slot + (wv + 32 * (i - MN) + frag_row) * kStageK + pos);
     };
-    auto multiply = [&](int half) {
-#pragma unroll
-        for (int i = 0; i < MV; ++i)
-#pragma unroll
-            for (int j = 0; j < MN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[half][i], fa[half][j], acc[i][j], 0, 0, 0);
+    auto multiply = [&](int half, int m) {
+        const int i = m / MN, j = m % MN;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[half][i], fa[half][j], acc[i][j], 0, 0, 0);
     };
+    // Of `work` pieces spread over `steps` steps, the first of step n.
+    auto share = [](int n, int steps, int work) { return (n * work + steps - 1) / steps; };
     for (int s = 0; s < stages; ++s) {
         // Stage s has landed once at most the RING - 2 stages after it are out;
         // past the barrier every wavefront has also read all of stage s - 1.
         stage_barrier<kLoads*(RING - 2)>();
-        issue(s + RING - 1);
-        read(s, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (s > 0)
-            multiply(1);
-        read(s, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(0);
+        constexpr int kFirst = kReads + kLoads;
+#pragma unroll
+        for (int m = 0; m < kMul; ++m) {
+            if (s > 0)
+                multiply(1, m);
+#pragma unroll
+            for (int p = share(m, kMul, kFirst); p < share(m + 1, kMul, kFirst); ++p) {
+                if (p < kReads)
+                    read(s, 0, p);
+                else
+                    issue(s + RING - 1, p - kReads);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int m = 0; m < kMul; ++m) {
+            multiply(0, m);
+#pragma unroll
+            for (int p = share(m, kMul, kReads); p < share(m + 1, kMul, kReads); ++p)
+                read(s, 1, p);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
-    multiply(1);
+#pragma unroll
+    for (int m = 0; m < kMul; ++m)
+        multiply(1, m);
     // No load may still be on its way into LDS when it is used again.
     stage_barrier<0>();
 
@@ -297,12 +360,11 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int at_v = 32 * i + 8 * e + 4 * (lane >> 5);
-                float z[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int v = v0 + wv + at_v + f;
-                    z[f] = static_cast<float>(acc[i][j][4 * e + f]) * sa * w_scale[v < cols ? v : cols - 1];
-                }
+                const float4 sw = *reinterpret_cast<const float4*>(scale_v + wv + at_v);
+                const float z[4] = {static_cast<float>(acc[i][j][4 * e]) * sa * sw.x,
+                                    static_cast<float>(acc[i][j][4 * e + 1]) * sa * sw.y,
+                                    static_cast<float>(acc[i][j][4 * e + 2]) * sa * sw.z,
+                                    static_cast<float>(acc[i][j][4 * e + 3]) * sa * sw.w};
                 int8_t* to = turn + (lane & 31) * kRowBytes + at_v * ESZ;
                 if constexpr (OUT == kBF16) {
                     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -397,10 +459,10 @@ int spec_int8_product(int rows, int depth, int cols, const int8_t* a, const floa
         !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(out, out_dtype == SPEC_BF16 ? 2 : 4))
         return SPEC_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    const long big = ((static_cast<long>(cols) + 255) / 256) * ((static_cast<long>(rows) + 127) / 128);
+    const long big = ((static_cast<long>(cols) + 255) / 256) * ((static_cast<long>(rows) + 255) / 256);
     hipError_t e;
     if (rows > 64 && big >= 256)
-        e = launch_tile<256, 128, 2, 2, 3>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s);
+        e = launch_tile<256, 256, 2, 4, 4>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s);
     else if (rows > 32)
         e = launch_tile<128, 64, 2, 2, 4>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s);
     else
