@@ -188,17 +188,15 @@ hipError_t launch_quantize(int rows, int cols, const void* x, int8_t* out_q, flo
 // v_mfma_i32_32x32x32_i8. The vocabulary is the M side: a lane then holds runs
 // of four consecutive outputs of one row.
 //
-// K in stages of 64 bytes through a ring of LDS slots, loaded straight into LDS
+// K in stages of BK bytes through a ring of LDS slots, loaded straight into LDS
 // RING - 1 stages ahead: one barrier per stage, after which the slot of the
-// stage before is refilled. A slot holds TV + TN rows of 64 bytes; a row's four
-// 16-byte chunks sit at positions XORed with (row / 4) % 4, so the sixteen rows
-// that a phase of a fragment read touches lie in sixteen different 16-byte
-// places of the 256 bytes of the banks ((row / 2) % 4 measured one conflict
-// cycle for every useful one).
+// stage before is refilled. A slot holds TV + TN rows of BK bytes; a row's
+// 16-byte chunks sit at positions XORed with the row's number in units of the
+// banks' 256 bytes (row / 4 for BK = 64), so the sixteen rows that a phase of a
+// fragment read touches lie in sixteen different 16-byte places of them (row / 2
+// for BK = 64 measured one conflict cycle for every useful one).
 // Rows past the end repeat the last one (their outputs are not stored), chunks
 // past the depth come from a page of zeros.
-constexpr int kStageK = 64;
-
 __device__ int4 zero_chunk;  // zero from load on, never written
 
 __device__ constexpr int wait_loads(int n) {
@@ -217,16 +215,21 @@ __device__ __forceinline__ void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
-template <int TV, int TN, int WV, int WN, int RING, int OUT>
+template <int TV, int TN, int WV, int WN, int BK, int RING, int OUT>
 __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
     const int8_t* __restrict__ a, const float* __restrict__ a_scale, const int8_t* __restrict__ w,
     const float* __restrict__ w_scale, int rows, int depth, int cols, int tiles_n, int tiles,
     void* __restrict__ out) {
     constexpr int kWavesHere = WV * WN;
     constexpr int MV = TV / WV / 32, MN = TN / WN / 32;
-    constexpr int kSlot = (TV + TN) * kStageK;
-    constexpr int kLoads = (TV + TN) / 16 / kWavesHere;  // 1 KiB each, per wavefront and stage
-    static_assert((TV + TN) / 16 % kWavesHere == 0, "every wavefront issues the same loads");
+    constexpr int kSlot = (TV + TN) * BK;
+    constexpr int kChunks = BK / 16;                  // of a row in a slot
+    constexpr int kRowsPerLoad = 64 / kChunks;        // a load covers 1 KiB
+    constexpr int kLoads = kSlot / 1024 / kWavesHere;  // per wavefront and stage
+    constexpr int kSteps = BK / 32;                   // of K = 32 each
+    static_assert(kSlot / 1024 % kWavesHere == 0, "every wavefront issues the same loads");
+    static_assert(kSteps % 2 == 0 && 256 % BK == 0, "two sets of fragments take turns");
+    auto swizzle = [](int row) { return row / (256 / BK) % kChunks; };
     // The epilogue turns a wavefront's 32 rows x 32 MV entries through LDS.
     constexpr int ESZ = OUT == kBF16 ? 2 : 4;
     constexpr int kRowBytes = 32 * MV * ESZ + 16;
@@ -253,8 +256,8 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
     int chunk[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int row = (wid + kWavesHere * i) * 16 + (lane >> 2);
-        chunk[i] = ((lane & 3) ^ ((row >> 2) & 3)) * 16;
+        const int row = (wid + kWavesHere * i) * kRowsPerLoad + lane / kChunks;
+        chunk[i] = (lane % kChunks ^ swizzle(row)) * 16;
         if (row < TV) {
             const int v = v0 + row;
             src[i] = w + static_cast<size_t>(v < cols ? v : cols - 1) * depth + chunk[i];
@@ -263,14 +266,14 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
             src[i] = a + static_cast<size_t>(n < rows ? n : rows - 1) * depth + chunk[i];
         }
     }
-    const int stages = (depth + kStageK - 1) / kStageK;
+    const int stages = (depth + BK - 1) / BK;
     const int8_t* zeros = reinterpret_cast<const int8_t*>(&zero_chunk);
     asm volatile("" : "+s"(zeros));  // looked up once, not in every stage
     auto issue = [&](int s, int i) {
         int8_t* slot = lds + (s % RING) * kSlot;
-        const int k = s * kStageK;
+        const int k = s * BK;
         // stages past the end load zeros into slots that nobody reads
-        const int8_t* from = k + kStageK <= depth || k + chunk[i] < depth ? src[i] + k : zeros;
+        const int8_t* from = k + BK <= depth || k + chunk[i] < depth ? src[i] + k : zeros;
         __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from),
                                          slot + (wid + kWavesHere * i) * 1024, 16, 0, 0);
     };
@@ -287,27 +290,28 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
             issue(s, i);
     const int wv = wid % WV * (TV / WV), wn = wid / WV * (TN / WN);
     const int frag_row = lane & 31;
-    const int swz = (frag_row >> 2) & 3;  // rows of a tile start at multiples of 32
-    // Half a stage (32 of K) is multiplied while the next half's fragments are
-    // read: of stage s - 1 the second half waits in registers over the barrier.
-    // The fragment reads and loads go between the matrix instructions, in whose
-    // shadow they issue: in one run before them, all wavefronts issue theirs
-    // together behind the barrier with the matrix cores idle (1486 us against
-    // 1380 at N = 2304, D = 4096, V = 152064).
+    const int swz = swizzle(frag_row);  // rows of a tile start at multiples of 32
+    // A step (32 of K) is multiplied while the next one's fragments are read: of
+    // stage s - 1 the last step waits in registers over the barrier. The fragment
+    // reads and loads go between the matrix instructions, in whose shadow they
+    // issue: in one run before them, all wavefronts issue theirs together behind
+    // the barrier with the matrix cores idle (1486 us against 1380 at N = 2304,
+    // D = 4096, V = 152064).
     constexpr int kReads = MV + MN, kMul = MV * MN;
     i32x4 fw[2][MV], fa[2][MN];
-    auto read = [&](int s, int half, int i) {
+    auto read = [&](int s, int step, int i) {
         const int8_t* slot = lds + (s % RING) * kSlot;
-        const int pos = ((2 * half + (lane >> 5)) ^ swz) * 16;
+        const int pos = ((2 * step + (lane >> 5)) ^ swz) * 16;
         if (i < MN)
-            fa[half][i] = *reinterpret_cast<const i32x4*>(slot + (TV + wn + 32 * i + frag_row) * kStageK + pos);
+            fa[step & 1][i] = *reinterpret_cast<const i32x4*>(slot + (TV + wn + 32 * i + frag_row) * BK + pos);
         else
-            fw[half][i - MN] =
-                *reinterpret_cast<const i32x4*>(slot + (wv + 32 * (i - MN) + frag_row) * kStageK + pos);
+            fw[step & 1][i - MN] =
+                *reinterpret_cast<const i32x4*>(slot + (wv + 32 * (i - MN) + frag_row) * BK + pos);
     };
-    auto multiply = [&](int half, int m) {
+    auto multiply = [&](int step, int m) {
         const int i = m / MN, j = m % MN;
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[half][i], fa[half][j], acc[i][j], 0, 0, 0);
+        acc[i][j] =
+            __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[step & 1][i], fa[step & 1][j], acc[i][j], 0, 0, 0);
     };
     // Of `work` pieces spread over `steps` steps, the first of step n.
     auto share = [](int n, int steps, int work) { return (n * work + steps - 1) / steps; };
@@ -315,27 +319,22 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
         // Stage s has landed once at most the RING - 2 stages after it are out;
         // past the barrier every wavefront has also read all of stage s - 1.
         stage_barrier<kLoads*(RING - 2)>();
-        constexpr int kFirst = kReads + kLoads;
 #pragma unroll
-        for (int m = 0; m < kMul; ++m) {
-            if (s > 0)
-                multiply(1, m);
+        for (int h = 0; h < kSteps; ++h) {
+            const int pieces = h == 0 ? kReads + kLoads : kReads;
 #pragma unroll
-            for (int p = share(m, kMul, kFirst); p < share(m + 1, kMul, kFirst); ++p) {
-                if (p < kReads)
-                    read(s, 0, p);
-                else
-                    issue(s + RING - 1, p - kReads);
+            for (int m = 0; m < kMul; ++m) {
+                if (h > 0 || s > 0)
+                    multiply(h + 1, m);  // the step before this one
+#pragma unroll
+                for (int p = share(m, kMul, pieces); p < share(m + 1, kMul, pieces); ++p) {
+                    if (p < kReads)
+                        read(s, h, p);
+                    else
+                        issue(s + RING - 1, p - kReads);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int m = 0; m < kMul; ++m) {
-            multiply(0, m);
-#pragma unroll
-            for (int p = share(m, kMul, kReads); p < share(m + 1, kMul, kReads); ++p)
-                read(s, 1, p);
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll
@@ -407,7 +406,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(
     }
 }
 
-template <int TV, int TN, int WV, int WN, int RING>
+template <int TV, int TN, int WV, int WN, int BK, int RING>
 hipError_t launch_tile(int rows, int depth, int cols, const int8_t* a, const float* a_scale,
                        const int8_t* w, const float* w_scale, int out_dtype, void* out, hipStream_t s) {
     const long tiles_v = (static_cast<long>(cols) + TV - 1) / TV;
@@ -416,11 +415,11 @@ hipError_t launch_tile(int rows, int depth, int cols, const int8_t* a, const flo
         return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(tiles_v * tiles_n)), block(64 * WV * WN);
     if (out_dtype == SPEC_BF16)
-        int8_product_kernel<TV, TN, WV, WN, RING, kBF16><<<grid, block, 0, s>>>(
+        int8_product_kernel<TV, TN, WV, WN, BK, RING, kBF16><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     else
-        int8_product_kernel<TV, TN, WV, WN, RING, kF32><<<grid, block, 0, s>>>(
+        int8_product_kernel<TV, TN, WV, WN, BK, RING, kF32><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     return hipGetLastError();
@@ -459,14 +458,29 @@ int spec_int8_product(int rows, int depth, int cols, const int8_t* a, const floa
         !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(out, out_dtype == SPEC_BF16 ? 2 : 4))
         return SPEC_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    const long big = ((static_cast<long>(cols) + 255) / 256) * ((static_cast<long>(rows) + 255) / 256);
+    auto tiles = [&](long tv, long tn) { return ((cols + tv - 1) / tv) * ((rows + tn - 1) / tn); };
+    // The largest tile that still gives the chip about enough workgroups
+    // (microseconds at D = 4096, V = 152064 unless another V and D stand there):
+    //   256 x 256, a workgroup per CU: 512 rows 325 (128 x 128: 404), 128 rows 197
+    //     (172); 512 rows of V = 32000, D = 2048, 250 tiles, 39 (47), of V = 8192,
+    //     64 tiles, 44 (128 x 64, 512 tiles: 25);
+    //   128 x 128: 128 rows 172 (128 x 64: 182); 256 rows of V = 32000, D = 2048,
+    //     500 tiles, 27 (37);
+    //   128 x 64: 64 rows 149 (64 x 32: 160); of V = 32000, D = 2048, 250 tiles,
+    //     17.3 (15.6);
+    //   64 x 32: 1 row 127 (128 x 64: 132), 16 rows of V = 8192 13.0 (20.2).
     hipError_t e;
-    if (rows > 64 && big >= 256)
-        e = launch_tile<256, 256, 2, 4, 4>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s);
-    else if (rows > 32)
-        e = launch_tile<128, 64, 2, 2, 4>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s);
+#define SPEC_TILE(...) \
+    e = launch_tile<__VA_ARGS__>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s)
+    if (rows > 128 && tiles(256, 256) >= 224)
+        SPEC_TILE(256, 256, 2, 4, 128, 2);
+    else if (rows > 64 && tiles(128, 128) >= 448)
+        SPEC_TILE(128, 128, 2, 2, 128, 2);
+    else if (rows > 32 && tiles(128, 64) >= 400)
+        SPEC_TILE(128, 64, 4, 1, 128, 2);
     else
-        e = launch_tile<128, 32, 2, 1, 4>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s);
+        SPEC_TILE(64, 32, 2, 1, 128, 3);
+#undef SPEC_TILE
     return e == hipSuccess ? SPEC_OK : e == hipErrorInvalidValue ? SPEC_EINVAL : SPEC_EHIP;
 }
 
