@@ -532,39 +532,72 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
 
 // ---------------------------------------------------------------- reorder ---
 
-// One thread owns one T-sized column of every slot of a (layer, sequence): it
-// reads the parents' columns before it writes any slot, so an in-place
-// permutation needs no other order.
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
+// In place: one thread owns one T-sized column of every slot of a (layer,
+// sequence), at most NB, and reads the parents' columns before it writes any
+// slot, so that a permutation needs no other order.
 template <typename T, int NB>
-__global__ __launch_bounds__(kBlock) void beam_reorder_kernel(
-    long states, int batch, int beams_in, int beams_out, const int32_t* __restrict__ parent,
-    const char* src, long src_stride, char* dst, long dst_stride, long cols, bool in_place) {
+__global__ __launch_bounds__(kBlock) void beam_reorder_kernel(long states, int batch, int beams,
+                                                              const int32_t* __restrict__ parent,
+                                                              char* state, long stride, long cols) {
     const long blocks_per = (cols + kBlock - 1) / kBlock;
+#pragma unroll 1
     for (long blk = blockIdx.x; blk < states * blocks_per; blk += gridDim.x) {
         const long lb = blk / blocks_per;
-        const long col = (blk % blocks_per) * kBlock + threadIdx.x;
+        const long col = (blk - lb * blocks_per) * kBlock + threadIdx.x;
         if (col >= cols)
             continue;
-        const int32_t* par = parent + (lb % batch) * beams_out;
-        const char* s = src + lb * beams_in * src_stride + col * static_cast<long>(sizeof(T));
-        char* d = dst + lb * beams_out * dst_stride + col * static_cast<long>(sizeof(T));
-        for (int j0 = 0; j0 < beams_out; j0 += NB) {
-            T r[NB] = {};
+        const int32_t* par = parent + (lb % batch) * beams;
+        char* s = state + lb * beams * stride + col * static_cast<long>(sizeof(T));
+        auto moves = [&](int j, int* w) {
+            *w = j < beams ? par[j] : -1;
+            return *w >= 0 && *w < beams && *w != j;
+        };
+        T r[NB] = {};
+        int w;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int w = j0 + j < beams_out ? par[j0 + j] : -1;
-                if (w >= 0 && w < beams_in && !(in_place && w == j0 + j))
-                    r[j] = *reinterpret_cast<const T*>(s + w * src_stride);
-            }
+        for (int j = 0; j < NB; ++j)
+            if (moves(j, &w))
+                r[j] = *reinterpret_cast<const T*>(s + w * stride);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int w = j0 + j < beams_out ? par[j0 + j] : -1;
-                if (w >= 0 && w < beams_in && !(in_place && w == j0 + j))
-                    *reinterpret_cast<T*>(d + (j0 + j) * dst_stride) = r[j];
-            }
-        }
+        for (int j = 0; j < NB; ++j)
+            if (moves(j, &w))
+                *reinterpret_cast<T*>(s + j * stride) = r[j];
+    }
+}
+
+// Into another array: a workgroup copies one run of kCopyUnroll * kBlock Ts of a
+// slot. Workgroups follow the destination's order, so that together they write
+// one advancing front (8 layers x 32 sequences x 8 beams of 512 KiB: 275 us, 7.8 TB/s
+// counting each slot's read though parents repeat; a workgroup per column of all
+// slots 476 us).
+constexpr int kCopyUnroll = 2;
+
+template <typename T>
+__global__ __launch_bounds__(kBlock) void beam_copy_kernel(
+    long states, int batch, int beams_in, int beams_out, const int32_t* __restrict__ parent,
+    const char* __restrict__ src, long src_stride, char* __restrict__ dst, long dst_stride, long cols,
+    long runs) {
+#pragma unroll 1
+    for (long blk = blockIdx.x; blk < states * beams_out * runs; blk += gridDim.x) {
+        const long slot = blk / runs, lb = slot / beams_out;
+        const int j = static_cast<int>(slot - lb * beams_out);
+        const int w = parent[(lb % batch) * beams_out + j];
+        if (w < 0 || w >= beams_in)
+            continue;
+        const long c0 = (blk - slot * runs) * (kCopyUnroll * kBlock) + threadIdx.x;
+        const T* s = reinterpret_cast<const T*>(src + (lb * beams_in + w) * src_stride);
+        T* d = reinterpret_cast<T*>(dst + slot * dst_stride);
+        T r[kCopyUnroll] = {};
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (c0 + u * kBlock < cols)
+                r[u] = s[c0 + u * kBlock];
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (c0 + u * kBlock < cols)
+                __builtin_nontemporal_store(r[u], d + c0 + u * kBlock);
     }
 }
 
@@ -573,19 +606,22 @@ hipError_t launch_reorder(long states, int batch, int beams_in, int beams_out,
                           const int32_t* parent, const void* src, long src_stride, void* dst,
                           long dst_stride, long bytes, bool in_place, hipStream_t stream) {
     const long cols = bytes / static_cast<long>(sizeof(T));
-    const long blocks = states * ((cols + kBlock - 1) / kBlock);
-    const dim3 grid(static_cast<unsigned>(blocks < (1L << 20) ? blocks : 1L << 20));
     const char* s = static_cast<const char*>(src);
     char* d = static_cast<char*>(dst);
-    // In place all slots of a column are in registers at once.
-#define SPEC_REORDER(NB)                                                                        \
-    beam_reorder_kernel<T, NB><<<grid, dim3(kBlock), 0, stream>>>(                              \
-        states, batch, beams_in, beams_out, parent, s, src_stride, d, dst_stride, cols, in_place)
+    auto grid = [](long blocks) { return dim3(static_cast<unsigned>(blocks < (1L << 23) ? blocks : 1L << 23)); };
+    if (!in_place) {
+        const long runs = (cols + kCopyUnroll * kBlock - 1) / (kCopyUnroll * kBlock);
+        beam_copy_kernel<T><<<grid(states * beams_out * runs), dim3(kBlock), 0, stream>>>(
+            states, batch, beams_in, beams_out, parent, s, src_stride, d, dst_stride, cols, runs);
+        return hipGetLastError();
+    }
+    const long blocks = states * ((cols + kBlock - 1) / kBlock);
+#define SPEC_REORDER(NB)                                                                  \
+    beam_reorder_kernel<T, NB><<<grid(blocks), dim3(kBlock), 0, stream>>>(                \
+        states, batch, beams_out, parent, d, dst_stride, cols)
     if (beams_out <= 4)
         SPEC_REORDER(4);
-    else if (beams_out <= 8 || !in_place)
-        SPEC_REORDER(8);
-    else if (beams_out <= 16)
+    else if (beams_out <= 16)  // (an instance of 8 takes three times its registers and is slower)
         SPEC_REORDER(16);
     else if (beams_out <= 32)
         SPEC_REORDER(32);
