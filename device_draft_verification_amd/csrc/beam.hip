@@ -28,10 +28,6 @@ namespace {
 
 constexpr int kPieceUnroll = 8;  // 16-byte groups of a piece per thread
 constexpr int kCollect = 256;    // collected entries: one per thread when ranked
-// Threads of a piece's workgroup. What a piece costs beside its loads is
-// collecting and ranking a little more than K entries: long lists take longer
-// pieces (K = 32 at V = 128256: PIECE_FIGURES).
-constexpr int piece_threads(int keep) { return keep <= 16 ? 256 : 512; }
 // log2(e) minus its binary32 rounding: the exponent's second term keeps the
 // normaliser's error at the rounding of single exponentials instead of 1.3e-8
 // times the distance from the row's maximum.
@@ -291,6 +287,7 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
         int place = kCollect;
         if ((tid & ~63) < held_keys) {  // wavefronts without an entry have nothing to rank
             place = 0;
+#pragma unroll 8
             for (int i = 0; i < held_keys; ++i)
                 place += list[i] > mine;
         }
@@ -344,7 +341,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     int pieces, const uint64_t* __restrict__ keys, const NormPart* __restrict__ norm,
     int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
     __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
-    __shared__ int alive[SPEC_BEAM_MAX], live[SPEC_BEAM_MAX], live_count;
+    __shared__ int alive[SPEC_BEAM_MAX];
     __shared__ int hist[kMergeThreads], wave_total[kMergeWaves], limit;
     __shared__ double wave_best[kMergeWaves];
     __shared__ Cand list[kCollect];
@@ -353,6 +350,25 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const long b = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const double none = -static_cast<double>(__builtin_huge_valf());
+    const int per_beam = pieces * keep, total = beams * per_beam;
+    const uint64_t* k_b = keys + b * total;
+    // Keys c0 + i * kMergeThreads, 0 past the end.
+    struct Chunk {
+        uint64_t key[kEntryChunk];
+        int beam[kEntryChunk];
+        double value[kEntryChunk];  // no candidate: none
+    };
+    auto load = [&](Chunk& x, int c0) {
+#pragma unroll
+        for (int i = 0; i < kEntryChunk; ++i) {
+            const int c = c0 + i * kMergeThreads;
+            x.key[i] = c < total ? k_b[c] : 0;
+            x.beam[i] = c < total ? c / per_beam : 0;
+        }
+    };
+    // The first keys are on their way while the beams' scores are read.
+    Chunk own;
+    load(own, tid);
     if (tid == 0) {
         count = 0;
         limit = kMergeThreads - 1;
@@ -397,29 +413,35 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         alive[tid] = is_finite_f32(sc) && is_finite_f64(l);
     }
     __syncthreads();
-    if (wid == 0) {  // the live beams, in order (at most 64)
-        const bool on = lane < beams && alive[lane];
-        const unsigned long long mask = __ballot(on);
-        if (on)
-            live[__popcll(mask & ((1ull << lane) - 1))] = lane;
-        if (lane == 0)
-            live_count = __popcll(mask);
-    }
-    __syncthreads();
-
-    const int per_beam = pieces * keep, total = live_count * per_beam;
-    const uint64_t* k_b = keys + b * beams * per_beam;
-    auto value_of = [&](uint64_t key, int w) {
-        return b_score[w] + (static_cast<double>(key_logit(key)) - b_lse[w]);
+    auto values = [&](Chunk& x) {
+#pragma unroll
+        for (int i = 0; i < kEntryChunk; ++i) {
+            const int w = x.beam[i];
+            x.value[i] = x.key[i] != 0 && alive[w]
+                             ? b_score[w] + (static_cast<double>(key_logit(x.key[i])) - b_lse[w])
+                             : none;
+        }
     };
-    // The best value: the pieces' lists are sorted, so among their first entries.
+    values(own);
+    // Every candidate of the sequence: a thread's first kEntryChunk from its
+    // registers, any further ones read again each time.
+    auto for_each = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < kEntryChunk; ++i)
+            if (own.value[i] > none)
+                f(Cand{own.value[i], own.key[i], own.beam[i]});
+        for (int c0 = tid + kEntryChunk * kMergeThreads; c0 < total; c0 += kEntryChunk * kMergeThreads) {
+            Chunk x;
+            load(x, c0);
+            values(x);
+#pragma unroll
+            for (int i = 0; i < kEntryChunk; ++i)
+                if (x.value[i] > none)
+                    f(Cand{x.value[i], x.key[i], x.beam[i]});
+        }
+    };
     double best = none;
-    for (int l = tid; l < live_count * pieces; l += kMergeThreads) {
-        const int w = live[l / pieces];
-        const uint64_t key = k_b[w * per_beam + l % pieces * keep];
-        if (key != 0)
-            best = fmax(best, value_of(key, w));
-    }
+    for_each([&](const Cand& x) { best = fmax(best, x.value); });
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         best = fmax(best, __shfl_xor(best, off, 64));
@@ -430,33 +452,15 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
 #pragma unroll
     for (int w = 1; w < kMergeWaves; ++w)
         best = fmax(best, wave_best[w]);
-
-    // Every entry of the live beams' lists, kEntryChunk of a thread's loads at a time.
-    auto for_each = [&](auto&& f) {
-        for (int c0 = tid; c0 < total; c0 += kEntryChunk * kMergeThreads) {
-            uint64_t key[kEntryChunk];
-            int beam[kEntryChunk];
-#pragma unroll
-            for (int i = 0; i < kEntryChunk; ++i) {
-                const int c = c0 + i * kMergeThreads;
-                const int at = c < total ? c : c0;
-                const int n = at / per_beam;
-                beam[i] = live[n];
-                key[i] = k_b[beam[i] * per_beam + at - n * per_beam];
-                if (c >= total)
-                    key[i] = 0;
-            }
-#pragma unroll
-            for (int i = 0; i < kEntryChunk; ++i)
-                if (key[i] != 0)
-                    f(Cand{value_of(key[i], beam[i]), key[i], beam[i]});
-        }
-    };
     auto bin_of = [&](double v) {
         return static_cast<int>(fminf(static_cast<float>(best - v) * kBinsPerUnit,
                                       static_cast<float>(kMergeThreads - 1)));
     };
-    for_each([&](const Cand& x) { atomicAdd(&hist[bin_of(x.value)], 1); });
+    for_each([&](const Cand& x) {
+        const int bin = bin_of(x.value);
+        if (bin < kMergeThreads - 1)  // nobody asks how many the last one holds
+            atomicAdd(&hist[bin], 1);
+    });
     __syncthreads();
     {
         int upto = hist[tid];
@@ -502,12 +506,16 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             if (tid < held)
                 mine = list[tid];
             place = 0;
+            int same = 0;
+#pragma unroll 8
             for (int i = 0; i < held; ++i) {
                 const double v = list[i].value;
                 place += v > mine.value;
-                if (v == mine.value)  // itself, and ties
-                    place += before(list[i], mine);
+                same += v == mine.value;
             }
+            if (same > 1)  // more than itself
+                for (int i = 0; i < held; ++i)
+                    place += list[i].value == mine.value && before(list[i], mine);
         }
         if (n <= kCollect) {
             if (tid < n) {
@@ -666,10 +674,10 @@ int spec_beam_init(int batch, int beams, int keep, int vocab, int dtype, void* h
     // and last groups may both hang over).
     const long W = dtype == SPEC_BF16 ? 8 : 4;
     const long groups = (static_cast<long>(vocab) + W - 1) / W + 1;
-    const long per_piece = static_cast<long>(kPieceUnroll) * piece_threads(keep);
+    const long per_piece = static_cast<long>(kPieceUnroll) * kBlock;
     const long pieces = (groups + per_piece - 1) / per_piece;
     const long rows = static_cast<long>(batch) * beams;
-    if (rows * pieces >= (1L << 32) / piece_threads(keep) || batch >= (1L << 32) / kMergeThreads || static_cast<long>(beams) * pieces * keep >= (1L << 30))
+    if (rows * pieces >= (1L << 32) / kBlock || batch >= (1L << 32) / kMergeThreads || static_cast<long>(beams) * pieces * keep >= (1L << 30))
         return SPEC_EINVAL;
     spec_beam_ctx* ctx = new (std::nothrow) spec_beam_ctx();
     if (!ctx)
@@ -715,28 +723,20 @@ int spec_beam_select(spec_beam_ctx* ctx, const void* logits, const float* score,
         return SPEC_EINVAL;
     const dim3 grid(static_cast<unsigned>(static_cast<long>(ctx->B) * ctx->W * ctx->pieces));
     hipStream_t s = ctx->stream;
-#define SPEC_PIECE(DT, T, NORM)                                                                \
-    beam_piece_kernel<DT, T, kPieceUnroll, NORM><<<grid, dim3(T), 0, s>>>(                     \
+#define SPEC_PIECE(DT, NORM)                                                                   \
+    beam_piece_kernel<DT, kBlock, kPieceUnroll, NORM><<<grid, dim3(kBlock), 0, s>>>(           \
         logits, score, lse, ctx->V, ctx->K, ctx->pieces, ctx->per_piece, ctx->keys, ctx->norm)
-#define SPEC_PIECE_T(DT, NORM)             \
-    if (piece_threads(ctx->K) == 256)      \
-        SPEC_PIECE(DT, 256, NORM);         \
-    else                                   \
-        SPEC_PIECE(DT, 512, NORM)
     if (ctx->dtype == SPEC_BF16) {
-        if (lse) {
-            SPEC_PIECE_T(kBF16, false);
-        } else {
-            SPEC_PIECE_T(kBF16, true);
-        }
+        if (lse)
+            SPEC_PIECE(kBF16, false);
+        else
+            SPEC_PIECE(kBF16, true);
     } else {
-        if (lse) {
-            SPEC_PIECE_T(kF32, false);
-        } else {
-            SPEC_PIECE_T(kF32, true);
-        }
+        if (lse)
+            SPEC_PIECE(kF32, false);
+        else
+            SPEC_PIECE(kF32, true);
     }
-#undef SPEC_PIECE_T
 #undef SPEC_PIECE
     if (hipGetLastError() != hipSuccess)
         return SPEC_EHIP;
