@@ -637,6 +637,8 @@ def _launch(func, device, stream, *args):
     if device != torch.cuda.current_device():
         raise ValueError(f"{func}: tensors on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
+        raise ValueError(f"{func}: tensors on cuda:{device}, the stream on {stream.device}")
     rc = getattr(_lib or load_library(), func)(
         *args, _current_stream(device) if stream is None else _stream_handle(stream))
     if rc < 0:

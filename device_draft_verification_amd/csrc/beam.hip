@@ -337,7 +337,7 @@ constexpr int kEntryChunk = 8;  // keys a thread has in flight
 
 template <bool NORM>
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
-    const float* __restrict__ score, const double* __restrict__ lse, int beams, int keep,
+    const float* score /* may be out_score */, const double* __restrict__ lse, int beams, int keep,
     int pieces, const uint64_t* __restrict__ keys, const NormPart* __restrict__ norm,
     int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
     __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
@@ -655,6 +655,7 @@ struct spec_beam_ctx {
     int B = 0, W = 0, K = 0, V = 0, dtype = 0, pieces = 0;
     int per_piece = 0;  // groups of a piece (the last has the rest)
     hipStream_t stream = nullptr;
+    int device = 0;
     void* ws = nullptr;
     uint64_t* keys = nullptr;
     NormPart* norm = nullptr;
@@ -690,6 +691,10 @@ int spec_beam_init(int batch, int beams, int keep, int vocab, int dtype, void* h
     ctx->pieces = static_cast<int>(pieces);
     ctx->per_piece = static_cast<int>(per_piece);
     ctx->stream = static_cast<hipStream_t>(hip_stream);
+    if (hipGetDevice(&ctx->device) != hipSuccess) {
+        delete ctx;
+        return SPEC_EHIP;
+    }
     const size_t key_bytes = static_cast<size_t>(rows) * pieces * keep * sizeof(uint64_t);
     const size_t norm_bytes = static_cast<size_t>(rows) * pieces * sizeof(NormPart);
     if (hipMalloc(&ctx->ws, key_bytes + norm_bytes) != hipSuccess) {
@@ -721,6 +726,11 @@ int spec_beam_select(spec_beam_ctx* ctx, const void* logits, const float* score,
         !aligned(out_parent, 4) || !aligned(out_token, 4) || !aligned(out_score, 4) ||
         (out_logq && !aligned(out_logq, 4)))
         return SPEC_EINVAL;
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess)
+        return SPEC_EHIP;
+    if (device != ctx->device)
+        return SPEC_ESTATE;
     const dim3 grid(static_cast<unsigned>(static_cast<long>(ctx->B) * ctx->W * ctx->pieces));
     hipStream_t s = ctx->stream;
 #define SPEC_PIECE(DT, NORM)                                                                   \

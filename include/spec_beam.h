@@ -26,9 +26,10 @@
  * temperature 1 (zeros when the logits are log-probabilities already). NULL:
  * the call forms lse[b][w] = log sum_v exp(z[b][w][v]) itself in the same pass
  * over the logits, exponentials in binary32 and sums in binary64, within
- * 2e-7 * (1 + |lse|) of the exact value; a beam with a NaN or +inf logit then
- * has no candidates. Two candidates of different beams whose values are closer
- * than that may then come in either order.
+ * 2^-23 (ln V + 6) of the exact value (as a rule a hundred times closer); a
+ * beam with a NaN or +inf logit then has no candidates. Two candidates of
+ * different beams whose values are closer than that may then come in either
+ * order (the same one on every call).
  *
  * Layouts: dense row-major DEVICE arrays owned by the caller: logits [B, W, V]
  * in the context's dtype (aligned to the element; any V), score [B, W]
@@ -39,7 +40,8 @@
  * Asynchrony and errors: as in spec_verify.h. spec_beam_select enqueues two
  * kernels on the context's stream and returns; it may be captured into a HIP
  * graph. Calls on one context share its workspace and must not overlap in
- * time, replays of graphs that captured it included.
+ * time, replays of graphs that captured it included. A context belongs to the
+ * device that was current when it was made: SPEC_ESTATE on another one.
  */
 #ifndef SPEC_BEAM_H
 #define SPEC_BEAM_H

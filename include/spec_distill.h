@@ -29,10 +29,12 @@
  * (gradient 0 there). A row with an id >= V, with a temperature that is not
  * positive and finite or whose reciprocal overflows, or whose lse is not finite
  * (no finite logit, a NaN or +inf logit) has loss, lse and its whole gradient
- * NaN; so does one whose teacher normaliser is not finite.
+ * NaN; so does one whose teacher normaliser or listed mass P is not finite (a
+ * NaN or +inf teacher logit).
  * Arithmetic: exponentials of the V student entries in binary32, their sums
  * in binary64 over binary32 sums of one 16-byte load; the list in binary64;
- * loss rounded once to binary32, gradients once to the logits' dtype.
+ * loss rounded once to binary32, gradients once to the logits' dtype. lse is
+ * within 2^-23 (ln V + 6) of the exact value.
  *
  * Layouts: dense row-major DEVICE arrays owned by the caller: logits, grad
  * [N, V] (SPEC_BF16 or SPEC_F32, aligned to the element, any V), ids [N, K]

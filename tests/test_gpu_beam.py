@@ -252,6 +252,57 @@ def test_step_replayed_from_a_graph():
         assert np.array_equal(state.cpu().numpy(), ops.beam_reorder(eager[0], before, before))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_entries_than_the_merge_keeps_in_registers(dtype):
+    """64 beams of several pieces: 12288 and more listed entries for one sequence, most of them far
+    below the best, and then all of them tied."""
+    logits, score = make(1, 64, 40000, dtype, seed=77)
+    lse = torch.logsumexp(logits.double(), -1)
+    check_given(logits, score, lse, 64, dtype)
+    check_given(logits, score * 0.01, lse, 64, dtype)
+    check_formed(logits, score, 64, dtype)
+    logits.zero_()
+    check_given(logits, torch.zeros_like(score), torch.zeros_like(lse), 64, dtype)
+
+
+def test_one_beam_far_ahead_of_the_others():
+    """All kept candidates from one beam; then from none but the last."""
+    logits, score = make(2, 16, 50000, "bf16", seed=78)
+    lse = torch.logsumexp(logits.double(), -1)
+    score.fill_(-1000.0)
+    score[:, 9] = -1.0
+    check_given(logits, score, lse, 32, "bf16")
+    score.fill_(-math.inf)
+    score[:, 15] = -3e38
+    check_given(logits, score, lse, 32, "bf16")
+
+
+def test_two_graphs_of_two_contexts_in_turn():
+    """Each captured selection has its own context's workspace: replays in turn do not disturb
+    each other."""
+    side = torch.cuda.Stream()
+    runs = []
+    for n in range(2):
+        logits, score = make(2, 4 + n, 20011, "bf16", seed=40 + n)
+        with torch.cuda.stream(side):
+            ctx = sv.spec_beam_init(2, 4 + n, 5, 20011, torch.bfloat16)
+        parent = torch.empty(2, 5, dtype=torch.int32, device="cuda")
+        token, sc = torch.empty_like(parent), torch.empty(2, 5, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            sv.spec_beam_select(ctx, logits, score, None, parent, token, sc)
+        runs.append((graph, ctx, logits, score, parent, token, sc))
+    want = [select(r[2], r[3], None, 5, "bf16") for r in runs]
+    for _ in range(4):
+        for r in runs:
+            r[0].replay()
+        torch.cuda.synchronize()
+        for r, w in zip(runs, want):
+            assert np.array_equal(r[4].cpu().numpy(), w[0]) and np.array_equal(r[5].cpu().numpy(), w[1])
+            assert np.array_equal(r[6].cpu().numpy(), w[2])
+
+
 def test_refusals_of_the_binding():
     logits, score = make(2, 3, 100, "f32", seed=1)
     ctx = sv.spec_beam_init(2, 3, 4, 100, torch.float32)

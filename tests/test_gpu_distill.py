@@ -301,6 +301,38 @@ def test_rows_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+def test_two_calls_at_once_on_two_streams():
+    ds = [make(30, 40009, 20, "bf16", seed=60 + n) for n in range(2)]
+    want = [call(d, 1) for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    outs = []
+    torch.cuda.synchronize()
+    for d, st in zip(ds, streams):
+        N, V = d["logits"].shape
+        o = (torch.empty(N, device="cuda"), torch.empty(N, dtype=torch.float64, device="cuda"),
+             torch.empty(N, V, dtype=torch.bfloat16, device="cuda"))
+        torch.cuda.synchronize()
+        sv.spec_distill_loss_grad(d["logits"], d["ids"], d["teacher"], d["teacher_lse"], d["temperature"],
+                                  d["weight"], *o, stream=st)
+        outs.append(o)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(np.array_equal(a.float().cpu().numpy() if a.dtype == torch.bfloat16 else a.cpu().numpy(), b,
+                                  equal_nan=True) for a, b in zip(o, w))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_that_rise_along_the_row(dtype):
+    """The running reference is moved again and again, and far-apart logits underflow."""
+    d = make(4, 70003, 12, dtype, seed=90)
+    d["logits"].copy_(torch.linspace(-300, 300, 70003))
+    for calls in (1, 2):
+        check(d, call(d, calls))
+    d["logits"].neg_()
+    for calls in (1, 2):
+        check(d, call(d, calls))
+
+
 def test_refusals_of_the_binding():
     d = make(3, 100, 4, "f32", seed=1)
     N, V = 3, 100

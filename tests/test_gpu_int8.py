@@ -115,6 +115,31 @@ def test_product(N, D, V, dtype):
     check_product(a, sa, w, sw, dtype, product(a, sa, w, sw, dtype))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,D,V", [
+    (33, 48, 51203), (64, 272, 51200),           # enough columns for tiles of 128 x 64
+    (65, 80, 57347), (128, 400, 57344),          # 128 x 128
+    (129, 16, 28673), (300, 144, 28675), (257, 1040, 28672), (512, 2064, 30008),   # 256 x 256
+])
+def test_product_in_the_larger_tiles(N, D, V, dtype):
+    print(f"\n[int8 N={N} D={D} V={V} {dtype}]", flush=True)
+    a, w = ints((N, D), N + D), ints((V, D), V + D + 1)
+    sa, sw = torch.rand(N, device="cuda") * 0.1, torch.rand(V, device="cuda") * 0.01
+    check_product(a, sa, w, sw, dtype, product(a, sa, w, sw, dtype))
+
+
+@pytest.mark.parametrize("N,V", [(64, 51203), (128, 57347), (300, 28675)])
+def test_the_larger_tiles_write_their_rows_only(N, V):
+    D = 32
+    a, w = ints((N, D), 3), ints((V, D), 4)
+    sa, sw = torch.rand(N, device="cuda"), torch.rand(V, device="cuda")
+    for offset in (0, 3):
+        buf = torch.full((N * V + offset + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        product(a, sa, w, sw, "bf16", buf[offset:offset + N * V].view(N, V))
+        check_product(a, sa, w, sw, "bf16", buf[offset:offset + N * V].view(N, V))
+        assert (buf[:offset] == 7).all() and (buf[offset + N * V:] == 7).all()
+
+
 @pytest.mark.parametrize("N", [1, 40, 300])
 def test_product_of_the_largest_magnitudes(N):
     """Every operand -128 at the largest depth: the sums come within 2^18 of 2^31."""
