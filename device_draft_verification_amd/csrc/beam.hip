@@ -71,8 +71,9 @@ __device__ inline int wave_sort(int v) {
 // The keep-th largest of the maxima of the workgroup's runs of G lanes (T / G of
 // them, at most 64), the same in every thread: a value belongs to the keep
 // largest when fewer than keep others are larger, and the smallest such value is
-// asked for. Every wavefront counts for itself, so one barrier does. lds: T / G values.
-template <int T, int G>
+// asked for. Every wavefront counts for itself, so one barrier does. Values are
+// BITS wide. lds: T / G values.
+template <int T, int G, int BITS>
 __device__ inline int kth_of_groups(int v, int keep, int* lds) {
     constexpr int N = T / G;
     static_assert(N <= 64 && 64 % N == 0, "one maximum per lane");
@@ -83,6 +84,21 @@ __device__ inline int kth_of_groups(int v, int keep, int* lds) {
         lds[threadIdx.x / G] = v;
     __syncthreads();
     v = lds[threadIdx.x % N];
+    if constexpr (N == 64) {
+        // One maximum per lane: the bits of the keep-th largest from the top, each
+        // by a ballot (counting larger ones costs two vector instructions for each
+        // of the 64). Of 32 bits the lowest 12 stay 0: that lowers the bar by less
+        // than 2^-11 of its value, and it lets no fewer entries through.
+        constexpr unsigned kZero = 1u << (BITS - 1);
+        const unsigned o = static_cast<unsigned>(v) + kZero;
+        unsigned t = 0;
+#pragma unroll
+        for (int bit = BITS - 1; bit >= (BITS == 32 ? 12 : 0); --bit) {
+            const unsigned up = t | 1u << bit;
+            t = __popcll(__ballot(o >= up)) >= keep ? up : t;
+        }
+        return static_cast<int>(t - kZero);
+    }
     int larger = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -131,12 +147,12 @@ __device__ inline int kth_of_threads(int v, int keep, int* lds) {
 // = 8) to 3.4 keep (16) entries through, of 64 maxima 1.4 keep (32), of the
 // threads' own 1.15 keep (64 of 256). The maxima cost a few lane exchanges and
 // one barrier, the threads' own a sort.
-template <int T>
+template <int T, int BITS>
 __device__ inline int bar_of(int v, int keep, int busy, int* lds) {
     if (keep <= 16 && busy >= T / 16 * keep)
-        return kth_of_groups<T, T / 16>(v, keep, lds);
+        return kth_of_groups<T, T / 16, BITS>(v, keep, lds);
     if (keep <= 48 && busy >= T / 64 * keep)
-        return kth_of_groups<T, T / 64>(v, keep, lds);
+        return kth_of_groups<T, T / 64, BITS>(v, keep, lds);
     return kth_of_threads<T>(v, keep, lds);
 }
 
@@ -217,7 +233,7 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
         }
     }
     const int held = g1 - g0;
-    const int bar = bar_of<T>(best, keep, held < T ? held : T, bars);
+    const int bar = bar_of<T, DT == kBF16 ? 16 : 32>(best, keep, held < T ? held : T, bars);
 
     repack(q);
     if constexpr (NORM) {
@@ -264,12 +280,26 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
     for (;;) {
         repack(q);
         const float bar_z = Row::from_order(bar_o);
+        // Hits are few and lie in different groups of different threads: each thread
+        // picks its own next group that has one, so that the wavefront goes round as
+        // often as its busiest thread, not once for every group with a hit anywhere.
+        unsigned groups = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (most[u] < bar_o)
-                continue;
+        for (int u = 0; u < U; ++u)
+            groups |= most[u] >= bar_o ? 1u << u : 0u;
+        while (groups) {
+            const int u = __builtin_ctz(groups);
+            groups &= groups - 1;
+            uint4 g = q[0];
+#pragma unroll
+            for (int i = 1; i < U; ++i) {
+                g.x = u == i ? q[i].x : g.x;
+                g.y = u == i ? q[i].y : g.y;
+                g.z = u == i ? q[i].z : g.z;
+                g.w = u == i ? q[i].w : g.w;
+            }
             float z[W];
-            Row::unpack(q[u], z);
+            Row::unpack(g, z);
             unsigned hits = 0;
 #pragma unroll
             for (int e = 0; e < W; ++e)
