@@ -170,12 +170,9 @@ __device__ __forceinline__ void repack(uint4 (&q)[U]) {
 //
 // 256 threads of eight 16-byte groups: 32 KiB of a row in 32 registers a thread,
 // enough workgroups per CU to load while others select. Bound by the read of the
-// logits for short lists (256 x 8 beams of 152064 bf16, K = 8: 83 us, 7.5 TB/s,
-// part of it from the last-level cache; 4 groups 99 us, 12 90 us), by the
-// vector instructions of the selection for longer ones (64 x 16 beams of 128256,
-// K = 32: 54 us, 4.9 TB/s, the vector units issuing in three cycles of four; 1024
-// threads to a piece 87 us). Small calls are a chain of latencies (4 beams of
-// 32000 floats: 6 us).
+// logits (256 x 8 beams of 152064 bf16, K = 8: 83 us, 7.5 TB/s, part of it from the
+// last-level cache; 4 groups 99 us, 12 90 us; 64 x 16 beams of 128256, K = 32: 38
+// us, 6.8 TB/s). Small calls are a chain of latencies (4 beams of 32000 floats: 6 us).
 template <int DT, int T, int U, bool NORM>
 __global__ __launch_bounds__(T) void beam_piece_kernel(
     const void* __restrict__ logits, const float* __restrict__ score,

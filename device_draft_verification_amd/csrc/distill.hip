@@ -118,7 +118,8 @@ __device__ inline RowList reduce_list(const DistillArgs& a, const ListFetch& f, 
     // which may take the logits' place.
     asm volatile("" : "+v"(mine.x));
     mine.x *= out.inv_t;
-    if (tid < SPEC_DISTILL_MAX_K) {
+    const bool holds = wid * 64 < a.top_k;  // the wavefront holds part of the list
+    if (holds) {
         const bool any_used = __ballot(used) != 0, any_out = __ballot(used && mine.id >= a.vocab) != 0,
                    any_mass = __ballot(used && !(y == -inf)) != 0;
         const float m = wave_max(y);
@@ -126,6 +127,10 @@ __device__ inline RowList reduce_list(const DistillArgs& a, const ListFetch& f, 
             lds.most[wid] = m;
             lds.flags[wid] = (any_used ? 1 : 0) | (any_out ? 2 : 0) | (any_mass ? 4 : 0);
         }
+    } else if (tid % 64 == 0 && tid < SPEC_DISTILL_MAX_K) {
+        lds.most[wid] = -inf;
+        lds.flags[wid] = 0;
+        lds.sum[wid] = lds.inner[wid] = 0.0;
     }
     lds_barrier();
     const int flags = lds.flags[0] | lds.flags[1] | lds.flags[2] | lds.flags[3];
@@ -136,7 +141,7 @@ __device__ inline RowList reduce_list(const DistillArgs& a, const ListFetch& f, 
                               : static_cast<double>(fmaxf(fmaxf(lds.most[0], lds.most[1]),
                                                           fmaxf(lds.most[2], lds.most[3])));
     double e = 0.0;
-    if (tid < SPEC_DISTILL_MAX_K) {
+    if (holds) {
         double t = 0.0;
         if (used) {
             const double d = static_cast<double>(y) - m;
@@ -370,8 +375,8 @@ __device__ inline char* grad_row(const DistillArgs& a, long row, const RowGroups
 // One workgroup per row, bound by the read of the logits (640 rows of 128256 bf16:
 // 33 us, 4.9 TB/s, 2.5 rows per CU). Few rows take 1024 threads each, for more loads
 // in flight; many take 512, so that one row's reductions hide behind another's
-// loads (both passes of 640 rows: 96 us; 1024 threads, 256, or 8 groups per thread
-// at a time cost 8 to 16 us more). 37 rows of 20011 floats: 7.7 us, latency.
+// loads (1024 threads, 256, or 8 groups per thread at a time cost 8 to 16 us
+// more). 37 rows of 20011 floats: 7.7 us, latency.
 template <int DT, int THREADS, int U>
 __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a) {
     using Row = RowGroups<DT>;
@@ -414,7 +419,7 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
 }
 
 // Every element is read, scaled and written once: bound by those two streams (640
-// rows of 128256 bf16: 65 us, 5.0 TB/s; the backward pass cannot keep what the
+// rows of 128256 bf16: 61 us, 5.4 TB/s; the backward pass cannot keep what the
 // forward pass read). Each workgroup reduces the row's list (at most 256 entries)
 // for itself while its part of the row is on its way.
 template <int DT, int THREADS, int U>
@@ -464,10 +469,12 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
 // 2304 rows of 152064 bf16 (1.4 GB read and written): 335-350 us, 4.0-4.2 TB/s; a
 // copy with one workgroup per row takes 267 us, one along a single front 217, and
 // the two passes apart 454. What is left over the copy is a row's own order: its
-// first gradient waits for its last logit, and two workgroups fit on a CU to
-// cover for each other, one row of 304 KB each in registers. (Workgroups that stay
-// for several rows and load the next row's groups as the gradients free their
-// registers: 339-381 us; 1024 threads of 19 groups spill.)
+// first gradient waits for its last logit, and a row of 304 KB in registers leaves
+// room for no second workgroup on the CU that would cover for the wait. (Workgroups
+// that stay for several rows and load the next row's groups as the gradients free
+// their registers: 339-381 us; 16 groups in registers and the rest read again, which
+// fits twice on a CU: 390; 20 groups so: 385; 1024 threads of 10 and the rest read
+// again: 419; 1024 threads of 19 groups spill.)
 constexpr int kTailUnroll = 4;
 
 template <int DT, int THREADS, int R, bool TAIL>
@@ -548,9 +555,11 @@ void launch_forward(int rows, const DistillArgs& a, hipStream_t s) {
 template <int DT>
 void launch_backward(int rows, const DistillArgs& a, hipStream_t s) {
     // One step of a workgroup's loads per split: workgroups follow the rows, so
-    // that together they read and write one advancing front (N = 640, V = 128256
-    // bf16, both passes: 96 us; 2048 workgroups with longer splits 100 us).
-    constexpr int kT = 256, kU = 4;
+    // that together they read and write one advancing front. Both passes of 640
+    // rows of 128256 bf16: 5 to 7 groups a thread 93 us, 4 96 us, 8 95 us, two steps
+    // of 4 96 us, 2048 workgroups with longer splits 100 us (shorter steps reduce
+    // the list more often, longer ones leave fewer workgroups to cover for it).
+    constexpr int kT = 256, kU = 5;
     const long groups = static_cast<long>(a.vocab) / RowGroups<DT>::W + 2;  // at any alignment
     const long steps = (groups + kT * kU - 1) / (kT * kU);
     const long most = ((1L << 32) / kT - 1) / rows;  // of one dispatch
