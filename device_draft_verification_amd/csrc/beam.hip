@@ -47,9 +47,10 @@ __device__ inline float unordered32(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// Key of a candidate; 0 marks no candidate (a finite z never has it).
+// Key of a candidate; 0 marks no candidate (a finite z never has it). Both zeros
+// are one logit: -0 + 0 is +0.
 __device__ inline uint64_t make_key(float z, int v) {
-    return static_cast<uint64_t>(ordered32(z)) << 32 | ~static_cast<uint32_t>(v);
+    return static_cast<uint64_t>(ordered32(z + 0.0f)) << 32 | ~static_cast<uint32_t>(v);
 }
 __device__ inline float key_logit(uint64_t k) { return unordered32(static_cast<uint32_t>(k >> 32)); }
 __device__ inline int key_token(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
@@ -271,7 +272,8 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
     // Collect the entries that reach the bar. If the list overflows (ties at the
     // bar, or a vocabulary whose best entries lie together), the keep-th largest
     // key that did fit is a higher bar, and keys are unique: again with that.
-    int bar_o = max(bar, Row::kOrderNegInf + 1);  // -inf is no candidate
+    auto with_zeros = [](int o) { return o == 0 ? -1 : o; };  // a bar at +0 lets -0 through
+    int bar_o = with_zeros(max(bar, Row::kOrderNegInf + 1));  // -inf is no candidate
     uint64_t bar_key = 0;
     const int v0 = static_cast<int>(r.element(g0 + tid));
     for (;;) {
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(T) void beam_piece_kernel(
             next_bar = mine;
         __syncthreads();
         bar_key = next_bar;
-        bar_o = Row::order_of(key_logit(bar_key));
+        bar_o = with_zeros(Row::order_of(key_logit(bar_key)));
         if (tid == 0)
             count = 0;
         __syncthreads();

@@ -160,6 +160,43 @@ def test_logits_of_one_beam_that_round_to_one_value():
     assert got[0].tolist() == [[0, 0, 0, 1, 1]] and got[1].tolist() == [[20, 30, 10, 20, 30]]
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 5, 16, 32, 64])
+@pytest.mark.parametrize("ones", [0, 3])
+def test_both_zeros_are_one_logit(ones, K, dtype):
+    B, W, V = 2, 3, 40009
+    g = torch.Generator().manual_seed(K)
+    pick = torch.rand(B, W, V, generator=g)
+    logits = torch.where(pick < 0.3, -0.0, torch.where(pick < 0.31, 0.0, -1.0))  # mostly -0 before +0
+    for n in range(ones):
+        logits[:, 1, 20000 + 7 * n] = 1.0
+    logits = logits.to(DTYPE[dtype]).cuda()
+    score, lse = torch.zeros(B, W, device="cuda"), torch.full((B, W), 10.0, dtype=torch.float64, device="cuda")
+    check_given(logits, score, lse, K, dtype)
+    logits = torch.where(pick < 0.001, -0.0, torch.where(pick < 0.002, 0.0, -1.0)).to(DTYPE[dtype]).cuda()
+    check_given(logits, score, lse, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [8, 20, 32, 48, 64])
+@pytest.mark.parametrize("scale", [1e-38, 1.0, 3.38e38])
+@pytest.mark.parametrize("sign", [-1.0, 0.0, 1.0])
+def test_logits_at_the_ends_of_the_type(sign, scale, K, dtype):
+    """All negative, of both signs, or all positive; tiny (with subnormals), ordinary, the largest."""
+    B, W, V = 2, 2, 17011
+    g = torch.Generator().manual_seed(K)
+    x = torch.rand(B, W, V, generator=g)
+    x = (2 * x - 1 if sign == 0 else sign * x) * scale
+    x[:, :, 5::11] = -math.inf
+    score, lse = torch.zeros(B, W, device="cuda"), torch.zeros(B, W, dtype=torch.float64, device="cuda")
+    logits = x.to(DTYPE[dtype]).cuda()
+    assert torch.isfinite(logits).any()
+    p, t, v, q = ops.beam_select(host(logits), score.cpu().numpy(), lse.cpu().numpy(), K)
+    got = select(logits, score, lse, K, dtype)
+    assert np.array_equal(got[0], p) and np.array_equal(got[1], t)
+    assert np.array_equal(got[2], v.astype(np.float32))
+
+
 def test_infinities_and_nan_are_no_candidates():
     for dtype in ("f32", "bf16"):
         logits, score = make(3, 4, 3001, dtype, seed=1)
