@@ -28,10 +28,6 @@ namespace {
 
 constexpr int kPieceUnroll = 8;  // 16-byte groups of a piece per thread
 constexpr int kCollect = 256;    // collected entries: one per thread when ranked
-// log2(e) minus its binary32 rounding: the exponent's second term keeps the
-// normaliser's error at the rounding of single exponentials instead of 1.3e-8
-// times the distance from the row's maximum.
-constexpr float kLog2eLow = 1.92596299e-8f;
 
 struct NormPart {
     float m;  // the piece's largest finite logit (-inf: none)

@@ -175,7 +175,12 @@ __device__ inline RowList reduce_list(const DistillArgs& a, const ListFetch& f, 
 // against the current reference, and only where that passes 2^8 a group the
 // reference is moved to the batch's maximum first. Terms then stay within 2^8
 // of 1, so the rounding of their exponents grows by at most 8 steps of 2^-24.
+// All of that holds while the reference, a rounded x log2e, is within a fraction
+// of the product: within 2^-2 below 2^22. References start at -2^22 or above, so
+// that what lies below adds nothing, and a row whose own largest entry lies
+// outside (its sum then misses in_reach) is summed by far_row instead.
 constexpr float kLazy = 256.0f;
+constexpr float kReach = 4194304.0f;
 
 template <int DT>
 __device__ inline float group_sum(const uint4& q, float inv_t, float ref) {
@@ -218,15 +223,29 @@ __device__ __forceinline__ void online_add(const uint4& q, float inv_t, float& r
 }
 
 // The first reference: the wavefront's largest entry of its first groups, or
-// none (kNegMax) where those hold nothing finite.
+// the least one allowed where those hold nothing above it.
 template <int DT>
 __device__ __forceinline__ float first_reference(const uint4& q, float inv_t) {
-    return fmaxf(kNegMax, scale_logit(wave_max(group_max<DT>(q)), inv_t) * kLog2e);
+    return fmaxf(-kReach, scale_logit(wave_max(group_max<DT>(q)), inv_t) * kLog2e);
 }
 
-// lse * log2e of the row from the threads' pairs. lds: 2 values per wavefront.
+// A row's sum against its largest reference: lse * log2e = top + log2(sum).
+struct RowSum {
+    double top, sum;
+};
+
+// The row's largest entry set the reference (its term is then within 2^-2 of 1
+// in the exponent) or lies at most 2^8 above the least one. A NaN fails.
+// The same in every thread, and made so for the compiler: a branch of single lanes
+// would keep the row's registers alive over far_row.
+__device__ inline bool in_reach(const RowSum& r) {
+    const bool in = r.top <= static_cast<double>(kReach) && r.sum >= 0.25 && is_finite_f64(r.sum);
+    return __builtin_amdgcn_readfirstlane(in) != 0;
+}
+
+// The row's sum from the threads' pairs. lds: 2 values per wavefront.
 template <int WAVES>
-__device__ inline double join(float ref, double s, double* lds) {
+__device__ inline RowSum join(float ref, double s, double* lds) {
     const float m = wave_max(ref);
     s = wave_sum(s * static_cast<double>(ref == m ? 1.0f : fast_exp2(ref - m)));
     if ((threadIdx.x & 63) == 0) {
@@ -244,7 +263,7 @@ __device__ inline double join(float ref, double s, double* lds) {
         const float d = static_cast<float>(lds[2 * w] - top);
         sum += lds[2 * w + 1] * static_cast<double>(fast_exp2(d));
     }
-    return top + log2(sum);
+    return RowSum{top, sum};
 }
 
 // ------------------------------------------------------------ the gradient ---
@@ -295,7 +314,8 @@ __device__ inline void store_group(const RowGroups<DT>& r, char* out, int g, boo
 }
 
 // The row's coefficients: exp(x - lse) = 2^(x log2e - ref) * 2^(ref - lse log2e),
-// the second factor (within a step of ref of 1) taken into the coefficient.
+// the second factor (within 2^-2 in the exponent below kReach) taken into the
+// coefficient.
 struct GradScale {
     float ref, dense;
     double coef;
@@ -345,10 +365,11 @@ __device__ inline void fill(const RowGroups<DT>& r, char* out, int g0, int g1, b
 }
 
 // The listed places, after the dense part: the first entry of an id writes the
-// sum over all entries of that id.
+// sum over all entries of that id. q: the student's probability at the thread's
+// own entry.
 template <int DT>
 __device__ inline void grad_list(const DistillArgs& a, const RowList& l, const Entry& mine,
-                                 const ListLds& lds, double lse, const GradScale& c, char* out) {
+                                 const ListLds& lds, double q, double coef, char* out) {
     double sum = 0.0;
     bool first = true;
     for (int j = 0; j < a.top_k; ++j) {
@@ -357,10 +378,8 @@ __device__ inline void grad_list(const DistillArgs& a, const RowList& l, const E
             first = first && j >= static_cast<int>(threadIdx.x);
         }
     }
-    if (first) {
-        const double q = exp(static_cast<double>(mine.x) - lse);
-        store_element<DT>(out, mine.id, static_cast<float>(c.coef * (l.mass * q - sum)));
-    }
+    if (first)
+        store_element<DT>(out, mine.id, static_cast<float>(coef * (l.mass * q - sum)));
 }
 
 template <int DT>
@@ -368,6 +387,97 @@ __device__ inline char* grad_row(const DistillArgs& a, long row, const RowGroups
     char* out = static_cast<char*>(a.out_grad) + row * static_cast<long>(a.vocab) * RowGroups<DT>::ESZ;
     *whole = (reinterpret_cast<uintptr_t>(out) & 15) == static_cast<uintptr_t>(r.shift) * RowGroups<DT>::ESZ;
     return out;
+}
+
+// ---------------------------------------------------------------- far rows ---
+
+// The largest, or the sum, of all threads' values, the same in every thread.
+template <int THREADS, bool MAX>
+__device__ inline double over_workgroup(double v, double* lds) {
+    // The lane's number under another name: exchange addresses that the wavefront
+    // sums above could share would stay in registers over the whole kernel.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const int2 b = __builtin_bit_cast(int2, v);
+        const int at = (lane ^ off) * 4;
+        const double o = __builtin_bit_cast(
+            double, make_int2(__builtin_amdgcn_ds_bpermute(at, b.x), __builtin_amdgcn_ds_bpermute(at, b.y)));
+        v = MAX ? fmax(v, o) : v + o;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w)
+        v = MAX ? fmax(v, lds[w]) : v + lds[w];
+    return v;
+}
+
+// A row whose largest scaled logit M lies so far out (a row masked with a large
+// finite constant) that M log2e has no digits left for the sum: everything is
+// taken against M itself, and M and log S = log sum exp(x - M) stay apart,
+//   q_v = exp(x_v - M) / S, loss = sum_j p_j (log p_j - (x_j - M)) + P log S,
+// one element at a time, by one workgroup, from memory: such rows are rare. Every
+// thread of the workgroup calls this, after reduce_list and before anything of the
+// row's gradient is written.
+template <int DT, int THREADS, bool LOSS, bool GRAD>
+__device__ inline void far_row(const DistillArgs& a, long row, const RowGroups<DT>& r, const RowList& l,
+                               const Entry& mine, const ListLds& list, double* lds, char* out) {
+    const int tid = threadIdx.x;
+    const float inf = __builtin_huge_valf(), nan = __builtin_nanf("");
+    float m = -inf;
+    bool wild = false;  // a NaN, or infinite above
+    for (long v = tid; v < r.vocab; v += THREADS) {
+        const float x = scale_logit(r.at(v), l.inv_t);
+        wild = wild || !(x < inf);
+        m = fmaxf(m, x);
+    }
+    const double top = over_workgroup<THREADS, true>(static_cast<double>(wild ? inf : m), lds);
+    m = static_cast<float>(top);
+    if (!is_finite_f64(top)) {
+        if (LOSS && tid == 0) {
+            a.out_loss[row] = nan;
+            a.out_lse[row] = static_cast<double>(nan);
+        }
+        if (GRAD)
+            for (long v = tid; v < r.vocab; v += THREADS)
+                store_element<DT>(out, v, nan);
+        return;
+    }
+    // exp(x - M); its second term keeps log2e's own rounding out of it
+    auto term = [&](long v) {
+        const float t = scale_logit(r.at(v), l.inv_t) - m;
+        return fast_exp2(__builtin_fmaf(t, kLog2e, t * kLog2eLow));
+    };
+    double s = 0.0;
+    for (long v = tid; v < r.vocab; v += THREADS)
+        s += static_cast<double>(term(v));
+    s = over_workgroup<THREADS, false>(s, lds);
+    if (LOSS) {
+        double t = 0.0;
+        const double p = mine.id >= 0 ? list.p[tid] : 0.0;
+        if (p > 0.0)
+            t = p * (log(p) - (static_cast<double>(mine.x) - top));
+        t = over_workgroup<THREADS, false>(t, lds);
+        const double log_s = log(s);
+        if (tid == 0) {
+            a.out_loss[row] = static_cast<float>(t + l.mass * log_s);
+            a.out_lse[row] = top + log_s;
+        }
+    }
+    if (GRAD) {
+        const double coef = static_cast<double>(a.weight[row]) * static_cast<double>(l.inv_t);
+        const double dense = coef * l.mass / s;
+        for (long v = tid; v < r.vocab; v += THREADS)
+            store_element<DT>(out, v, static_cast<float>(dense * static_cast<double>(term(v))));
+        __syncthreads();  // the dense part is written
+        if (mine.id >= 0)
+            grad_list<DT>(a, l, mine, list, exp(static_cast<double>(mine.x) - top) / s, coef, out);
+    }
 }
 
 // ----------------------------------------------------------------- kernels ---
@@ -410,11 +520,15 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
             break;
         r.template load<U, THREADS>(g0, tid, r.groups, q);
     }
-    const double lse = join<THREADS / 64>(ref, s, lds) / static_cast<double>(kLog2e);
+    const RowSum w = join<THREADS / 64>(ref, s, lds);
+    if (!in_reach(w)) {
+        far_row<DT, THREADS, true, false>(a, row, r, l, mine, list, lds, nullptr);
+        return;
+    }
+    const double lse = (w.top + log2(w.sum)) / static_cast<double>(kLog2e);
     if (tid == 0) {
-        const bool ok = is_finite_f64(lse);
-        a.out_loss[row] = ok ? static_cast<float>(l.inner + l.mass * lse) : nan;
-        a.out_lse[row] = ok ? lse : static_cast<double>(nan);
+        a.out_loss[row] = static_cast<float>(l.inner + l.mass * lse);
+        a.out_lse[row] = lse;
     }
 }
 
@@ -426,6 +540,7 @@ template <int DT, int THREADS, int U>
 __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a, int splits, int per_split) {
     using Row = RowGroups<DT>;
     __shared__ ListLds list;
+    __shared__ double lds[THREADS / 64];
     const int tid = threadIdx.x;
     const long row = blockIdx.x / static_cast<unsigned>(splits);
     const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(splits));
@@ -445,7 +560,15 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
         fill<DT, THREADS>(r, out, g0, g1, whole, l.empty ? 0.0f : __builtin_nanf(""));
         return;
     }
-    const GradScale c = grad_scale(a.weight[row], l, lse * static_cast<double>(kLog2e));
+    const double lse2 = lse * static_cast<double>(kLog2e);
+    // The normaliser has lost its logarithm of the sum, or soon will have: formed
+    // again, by one workgroup for the whole row (which may be its own gradient).
+    if (!(fabs(lse2) <= static_cast<double>(kReach))) {
+        if (part == 0)
+            far_row<DT, THREADS, false, true>(a, row, r, l, mine, list, lds, out);
+        return;
+    }
+    const GradScale c = grad_scale(a.weight[row], l, lse2);
     for (int g = g0;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -460,7 +583,7 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
     if (mine.id >= 0) {
         const long at = (mine.id + r.shift) / Row::W;
         if (at >= g0 && at < g1)
-            grad_list<DT>(a, l, mine, list, lse, c, out);
+            grad_list<DT>(a, l, mine, list, exp(static_cast<double>(mine.x) - lse), c.coef, out);
     }
 }
 
@@ -494,7 +617,7 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     r.template load<R, THREADS, true>(0, tid, r.groups, q);
     const RowList l = reduce_list(a, f, mine, list);
     const float nan = __builtin_nanf("");
-    float ref = kNegMax;
+    float ref = -kReach;
     double s = 0.0;
     if (!l.empty && !l.bad) {
         ref = first_reference<DT>(q[0], l.inv_t);
@@ -510,15 +633,19 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
                     online_add<DT>(t[u], l.inv_t, ref, s);
             }
     }
-    const double lse2 = join<THREADS / 64>(ref, s, lds);
+    const RowSum w = join<THREADS / 64>(ref, s, lds);
+    const double lse2 = w.top + log2(w.sum);
     const double lse = lse2 / static_cast<double>(kLog2e);
-    const bool bad = l.bad || !is_finite_f64(lse);
-    if (tid == 0) {
-        a.out_loss[row] = l.empty ? 0.0f : bad ? nan : static_cast<float>(l.inner + l.mass * lse);
-        a.out_lse[row] = l.empty || bad ? static_cast<double>(nan) : lse;
+    const bool none = l.empty || l.bad, far = !none && !in_reach(w);
+    if (tid == 0 && !far) {
+        a.out_loss[row] = l.empty ? 0.0f : l.bad ? nan : static_cast<float>(l.inner + l.mass * lse);
+        a.out_lse[row] = none ? static_cast<double>(nan) : lse;
     }
-    if (l.empty || bad) {
-        fill<DT, THREADS>(r, out, 0, r.groups, whole, l.empty ? 0.0f : nan);
+    if (none || far) {
+        if (far)
+            far_row<DT, THREADS, true, true>(a, row, r, l, mine, list, lds, out);
+        else
+            fill<DT, THREADS>(r, out, 0, r.groups, whole, l.empty ? 0.0f : nan);
         return;
     }
     const GradScale c = grad_scale(a.weight[row], l, lse2);
@@ -541,7 +668,7 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     }
     __syncthreads();  // the dense part is written
     if (mine.id >= 0)
-        grad_list<DT>(a, l, mine, list, lse, c, out);
+        grad_list<DT>(a, l, mine, list, exp(static_cast<double>(mine.x) - lse), c.coef, out);
 }
 
 template <int DT>

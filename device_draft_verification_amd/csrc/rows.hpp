@@ -11,6 +11,11 @@
 
 namespace specv {
 
+// log2(e) minus its binary32 rounding: the exponent's second term keeps the
+// normaliser's error at the rounding of single exponentials instead of 1.3e-8
+// times the distance from the row's maximum.
+constexpr float kLog2eLow = 1.92596299e-8f;
+
 template <int DT>
 struct RowGroups {
     static constexpr int W = DT == kBF16 ? 8 : 4;

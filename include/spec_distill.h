@@ -34,7 +34,13 @@
  * Arithmetic: exponentials of the V student entries in binary32, their sums
  * in binary64 over binary32 sums of one 16-byte load; the list in binary64;
  * loss rounded once to binary32, gradients once to the logits' dtype. lse is
- * within 2^-23 (ln V + 6) of the exact value.
+ * within 2^-23 (ln V + 6) of the exact value, plus its own rounding to binary64.
+ * Far rows: any finite scaled logits are allowed. A row whose largest one is
+ * beyond +-2.9e6 (2^22 / log2 e; a row masked throughout with a large finite
+ * constant) is formed in binary64 against that largest logit, which takes one
+ * workgroup several passes over the row. So large an lse no longer holds the
+ * logarithm of the sum to the bound above, or at all: the backward call takes
+ * from it only that the row is far, and forms the sum again from the logits.
  *
  * Layouts: dense row-major DEVICE arrays owned by the caller: logits, grad
  * [N, V] (SPEC_BF16 or SPEC_F32, aligned to the element, any V), ids [N, K]
