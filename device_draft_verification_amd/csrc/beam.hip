@@ -368,6 +368,10 @@ constexpr int kMergeWaves = kMergeThreads / 64;
 // The last bin holds everything 16 or more below.
 constexpr float kBinsPerUnit = 32.0f;
 constexpr int kEntryChunk = 8;  // keys a thread has in flight
+// A formed normaliser beyond this (a beam masked with a large finite constant) has
+// lost too much of its logarithm: its largest logit and the logarithm stay apart.
+// Below it binary64's own rounding is 2^-31 at most.
+constexpr double kFarNormaliser = 4194304.0;
 
 // The K best of a sequence's beams * pieces * K keys. One workgroup per sequence:
 // the keys are few (16 beams x 8 pieces x 32 of 64 sequences: 2 MB beside the logits' 263),
@@ -380,6 +384,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     int pieces, const uint64_t* __restrict__ keys, const NormPart* __restrict__ norm,
     int32_t* out_parent, int32_t* out_token, float* out_score, float* out_logq) {
     __shared__ double b_score[SPEC_BEAM_MAX], b_lse[SPEC_BEAM_MAX];
+    __shared__ double b_off[NORM ? SPEC_BEAM_MAX : 1];  // taken from a beam's logits first
     __shared__ int alive[SPEC_BEAM_MAX];
     __shared__ int hist[kMergeThreads], wave_total[kMergeWaves], limit;
     __shared__ double wave_best[kMergeWaves];
@@ -438,9 +443,11 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
             for (int off = 1; off < 16; off <<= 1)
                 s += __shfl_xor(s, off, 64);
             if ((tid & 15) == 0) {
-                const double l = static_cast<double>(m) + log(s);
+                const double log_s = log(s), l = static_cast<double>(m) + log_s;
+                const bool far = fabs(l) > kFarNormaliser;
                 b_score[w] = static_cast<double>(sc);
-                b_lse[w] = l;
+                b_off[w] = far ? static_cast<double>(m) : 0.0;
+                b_lse[w] = far ? log_s : l;
                 alive[w] = ok && is_finite_f64(l);
             }
         }
@@ -452,12 +459,19 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         alive[tid] = is_finite_f32(sc) && is_finite_f64(l);
     }
     __syncthreads();
+    auto logq = [&](uint64_t key, int w) {
+        const double z = static_cast<double>(key_logit(key));
+        if constexpr (NORM)
+            return (z - b_off[w]) - b_lse[w];
+        else
+            return z - b_lse[w];
+    };
     auto values = [&](Chunk& x) {
 #pragma unroll
         for (int i = 0; i < kEntryChunk; ++i) {
             const int w = x.beam[i];
             x.value[i] = x.key[i] != 0 && alive[w]
-                             ? b_score[w] + (static_cast<double>(key_logit(x.key[i])) - b_lse[w])
+                             ? b_score[w] + logq(x.key[i], w)
                              : none;
         }
     };
@@ -524,8 +538,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
         out_token[at] = some ? key_token(x.key) : -1;
         out_score[at] = some ? static_cast<float>(x.value) : -__builtin_huge_valf();
         if (out_logq)
-            out_logq[at] = some ? static_cast<float>(static_cast<double>(key_logit(x.key)) - b_lse[x.beam])
-                                : -__builtin_huge_valf();
+            out_logq[at] = some ? static_cast<float>(logq(x.key, x.beam)) : -__builtin_huge_valf();
     };
     Cand bar{none, 0, SPEC_BEAM_MAX};  // behind every candidate
     for (;;) {

@@ -26,7 +26,9 @@
  * temperature 1 (zeros when the logits are log-probabilities already). NULL:
  * the call forms lse[b][w] = log sum_v exp(z[b][w][v]) itself in the same pass
  * over the logits, exponentials in binary32 and sums in binary64, within
- * 2^-23 (ln V + 6) of the exact value (as a rule a hundred times closer); a
+ * 2^-23 (ln V + 6) of the exact value (as a rule a hundred times closer; one
+ * beyond +-2^22, of a beam masked with a large finite constant, stays apart as
+ * M + log S with M the beam's largest logit, and logq is (z - M) - log S); a
  * beam with a NaN or +inf logit then has no candidates. Two candidates of
  * different beams whose values are closer than that may then come in either
  * order (the same one on every call).
