@@ -581,7 +581,7 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
     }
     __syncthreads();  // the dense part is written
     if (mine.id >= 0) {
-        const long at = (mine.id + r.shift) / Row::W;
+        const long at = r.group_of(mine.id);
         if (at >= g0 && at < g1)
             grad_list<DT>(a, l, mine, list, exp(static_cast<double>(mine.x) - lse), c.coef, out);
     }

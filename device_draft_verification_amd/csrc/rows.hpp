@@ -50,6 +50,9 @@ struct RowGroups {
     // First element of group g (may lie outside the row at its ends).
     __device__ long element(int g) const { return static_cast<long>(g) * W - shift; }
 
+    // The group that holds element v of the row (in 64 bits: their sum may pass 2^31).
+    __device__ long group_of(int v) const { return (static_cast<long>(v) + shift) / W; }
+
     __device__ bool inside(int g) const { return g >= full0 && g < full1; }
 
     // A group at an end of the row, -inf outside the row.
