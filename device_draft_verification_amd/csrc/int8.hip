@@ -170,15 +170,18 @@ hipError_t launch_quantize(int rows, int cols, const void* x, int8_t* out_q, flo
     quantize_rows_kernel<DT, T, U, LONG><<<dim3(rows), dim3(T), 0, s>>>(x, cols, out_q, out_scale)
     // Two groups per thread: enough loads in flight, and short chains of
     // quotients (2304 rows of 4096 bf16: 8 us; four per thread 10, eight 14).
+    // So many rows that one dispatch does not hold the wider workgroups (2^32
+    // work-items) take the narrow one that reads a row twice.
+    auto fits = [&](long threads) { return rows * threads < (1L << 32); };
     if (groups <= 128)
         SPEC_QUANTIZE(64, 2, false);
     else if (groups <= 256)
         SPEC_QUANTIZE(128, 2, false);
     else if (groups <= 512)
         SPEC_QUANTIZE(256, 2, false);
-    else if (groups <= 1024)
+    else if (groups <= 1024 && fits(512))
         SPEC_QUANTIZE(512, 2, false);
-    else if (groups <= 2048)
+    else if (groups <= 2048 && fits(1024))
         SPEC_QUANTIZE(1024, 2, false);
     else
         SPEC_QUANTIZE(256, 8, true);

@@ -27,7 +27,10 @@
  * x in `dtype` (SPEC_F32 or SPEC_BF16, aligned to the element), any D >= 1.
  * spec_int8_product: D % 16 == 0, 16 <= D <= SPEC_INT8_MAX_DEPTH (the sum
  * stays inside int32), a and w 16-byte aligned; out aligned to its element, any
- * V >= 1. N >= 0. Outputs must not overlap inputs.
+ * V >= 1. N >= 0. Outputs must not overlap inputs. One dispatch limits the
+ * sizes: N < 2^24 rows in spec_quantize_rows; in spec_int8_product the tiles of
+ * the output, which every output that fits the card's memory stays below (N <
+ * 2^31 - 256 for the narrowest). SPEC_EINVAL beyond.
  *
  * Asynchrony and errors: as in spec_verify.h; each call enqueues one kernel on
  * hip_stream (a hipStream_t, NULL = the null stream), needs no workspace, and

@@ -49,3 +49,29 @@ def test_distillation_of_the_longest_row(calls):
     for part in out[0].split(1 << 29):
         assert abs(part.max().item() - q) <= q * 2.0 ** -7 and abs(part.min().item() - q) <= q * 2.0 ** -7
     assert (grad[:off] == 7).all() and (grad[off + V:] == 7).all()
+
+
+def test_quantisation_of_so_many_rows_that_wide_workgroups_do_not_fit():
+    """2^22 rows that 1024 threads would each take: one dispatch does not hold 2^32 work-items."""
+    N, D, step = 1 << 22, 8200, 1 << 16
+    print("\n[quantise 2^22 rows]", flush=True)
+    x = torch.empty(N, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    for n in range(0, N, step):
+        x[n:n + step].normal_(0, 1 + n / N, generator=g)
+    q = torch.full((N, D), 99, dtype=torch.int8, device="cuda")
+    scale = torch.full((N,), 7.0, device="cuda")
+    sv.spec_quantize_rows(x, q, scale)
+    torch.cuda.synchronize()
+    wrong_scales, wrong_bytes = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for n in range(0, N, step):
+        part, s = x[n:n + step], scale[n:n + step]
+        # in binary64, rounded once: torch divides by a number through its reciprocal
+        wrong_scales += (s != (part.abs().amax(1).double() / 127).float()).sum()
+        # the bytes of the first and last 2^12 rows of each 2^16
+        for a in (0, step - 4096):
+            rows = slice(a, a + 4096)
+            want = (part[rows].double() / s[rows].double()[:, None]).round().clamp(-127, 127)
+            wrong_bytes += (want != q[n:n + step][rows]).sum()
+    assert wrong_scales.item() == 0 and wrong_bytes.item() == 0
