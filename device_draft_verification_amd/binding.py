@@ -629,6 +629,15 @@ def _arg(t, shape, dtype, name, device):
     return t.data_ptr()
 
 
+def _refuse_other_device(func, device, stream):
+    """A stream that work on `device` cannot run on; None is the current device's own."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != device:
+        raise ValueError(f"{func}: the device is cuda:{device}, the stream on {stream.device}")
+    if stream is None and device != torch.cuda.current_device():
+        raise ValueError(f"{func}: the device is cuda:{device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
 def _launch(func, device, stream, *args):
     """Call the library's `func`, which launches on the current device's stream: the tensors'
     device has to be that one."""
@@ -665,13 +674,16 @@ class BeamContext:
 
 def spec_beam_init(batch: int, beams: int, keep: int, vocab: int, dtype, stream=None) -> BeamContext:
     code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    device = torch.cuda.current_device()
+    _refuse_other_device("spec_beam_init", device, stream)
     h = ctypes.c_void_p()
     _check("spec_beam_init", load_library().spec_beam_init(
         batch, beams, keep, vocab, code, _stream_handle(stream), ctypes.byref(h)))
-    return BeamContext(h, batch, beams, keep, vocab, code, torch.cuda.current_device())
+    return BeamContext(h, batch, beams, keep, vocab, code, device)
 
 
 def spec_beam_set_stream(ctx: BeamContext, stream=None) -> None:
+    _refuse_other_device("spec_beam_set_stream", ctx.device, stream)
     _check("spec_beam_set_stream",
            load_library().spec_beam_set_stream(ctx.handle, _stream_handle(stream)))
 

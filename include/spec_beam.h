@@ -43,7 +43,8 @@
  * kernels on the context's stream and returns; it may be captured into a HIP
  * graph. Calls on one context share its workspace and must not overlap in
  * time, replays of graphs that captured it included. A context belongs to the
- * device that was current when it was made: SPEC_ESTATE on another one.
+ * device that was current when it was made: SPEC_ESTATE on another one. Its
+ * streams have to be that device's.
  */
 #ifndef SPEC_BEAM_H
 #define SPEC_BEAM_H
