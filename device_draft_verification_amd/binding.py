@@ -683,6 +683,8 @@ def spec_beam_init(batch: int, beams: int, keep: int, vocab: int, dtype, stream=
 
 
 def spec_beam_set_stream(ctx: BeamContext, stream=None) -> None:
+    """Later selections of this context run on `stream` (None: the current one). What the
+    earlier stream still holds has to be waited for first: they share the workspace."""
     _refuse_other_device("spec_beam_set_stream", ctx.device, stream)
     _check("spec_beam_set_stream",
            load_library().spec_beam_set_stream(ctx.handle, _stream_handle(stream)))
@@ -693,7 +695,10 @@ def spec_beam_select(ctx: BeamContext, logits, score, lse, out_parent, out_token
     """The `keep` best continuations over beams and vocabulary: logits [B, W, V] in the
     context's dtype, score [B, W] float32 (-inf: no beam), lse [B, W] float64 row
     normalisers or None (formed by the call); out_parent, out_token [B, K] int32,
-    out_score, out_logq [B, K] float32 (out_logq may be None). Runs on the context's stream."""
+    out_score, out_logq [B, K] float32 (out_logq may be None). Runs on the context's stream:
+    the one it was made with, or that spec_beam_set_stream gave it since, whatever stream is
+    current. Calls that read the outputs on another stream (spec_beam_reorder takes the current
+    one) have to be ordered behind it."""
     B, W, K, dev = ctx.batch, ctx.beams, ctx.keep, ctx.device
     i32, f32 = torch.int32, torch.float32
     rc = (_lib or load_library()).spec_beam_select(
@@ -719,7 +724,8 @@ def spec_beam_reorder(parent, src, dst, used_bytes: int | None = None, stream=No
     """dst[l, b, j] = src[l, b, parent[b, j]] for parents inside src's beams, other slots left
     as they are: parent [B, K] int32, src [L, B, W, ...] and dst [L, B, K, ...] of one dtype
     and state shape; dst may be src (reordered in place). used_bytes moves a prefix of each
-    state only."""
+    state only. Runs on `stream`, or the current one: behind the selection that wrote `parent`
+    only if that ran on the same stream or was waited for."""
     if src.dim() < 3 or dst.dim() != src.dim():
         raise ValueError("src and dst are [layers, batch, beams, ...]")
     shape, dev = src.shape, src.get_device()

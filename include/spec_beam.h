@@ -42,7 +42,8 @@
  * Asynchrony and errors: as in spec_verify.h. spec_beam_select enqueues two
  * kernels on the context's stream and returns; it may be captured into a HIP
  * graph. Calls on one context share its workspace and must not overlap in
- * time, replays of graphs that captured it included. A context belongs to the
+ * time, replays of graphs that captured it included. The reordering takes its
+ * stream as an argument: give it the context's, or order the two. A context belongs to the
  * device that was current when it was made: SPEC_ESTATE on another one. Its
  * streams have to be that device's.
  */
