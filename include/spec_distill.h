@@ -5,8 +5,15 @@
  * The operation: a draft model is worth what the verifier accepts of it, and
  * acceptance is 1 - TV(p, q) (see spec_verify.h): a draft is trained towards
  * the target's distribution. Of the target only the top entries of each row
- * are kept (the lists of spec_verify_outcomes, or a top-k of its logits); the
- * loss is the Kullback-Leibler divergence of the draft's row from that list.
+ * are kept (a top-k of its logits); the loss is the Kullback-Leibler divergence
+ * of the draft's row from that list.
+ * The lists of spec_verify_outcomes hold probabilities, not logits, and for
+ * every length below G those of the residual max(0, p - q), which is no teacher
+ * for the draft. The list of length G is the target's own row: its tokens are
+ * the ids, the logarithms of its probabilities the teacher logits, with
+ * teacher_lse 0 (they are normalised over the whole vocabulary) and temperature
+ * 1 (or T times the logarithms with temperature T, where the draft's row is
+ * scaled by T as well).
  *
  * Precise definition, per row n with T = temperature[n], r = fl32(1/T):
  *   x_v = fl32(z[n][v] * r)              the draft's (student's) scaled logits
