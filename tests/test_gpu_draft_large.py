@@ -75,3 +75,48 @@ def test_quantisation_of_so_many_rows_that_wide_workgroups_do_not_fit():
             want = (part[rows].double() / s[rows].double()[:, None]).round().clamp(-127, 127)
             wrong_bytes += (want != q[n:n + step][rows]).sum()
     assert wrong_scales.item() == 0 and wrong_bytes.item() == 0
+
+
+def test_distillation_in_two_calls_past_32_bit_offsets():
+    """Rows whose elements start more than 2^32 bytes behind the first, through the forward pass and
+    the backward pass with its rows and parts of rows."""
+    N, V = 12, 200_000_000
+    print("\n[distill two calls, 12 x 2e8]", flush=True)
+    z = torch.zeros(N, V, dtype=torch.bfloat16, device="cuda")
+    z[:, V // 2:] = 1.0
+    grad = torch.full((N, V), 7.0, dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((N, 1), V - 1, dtype=torch.int32, device="cuda")
+    f = lambda v, dt=torch.float32: torch.full((N,), v, dtype=dt, device="cuda")
+    loss, lse = f(0.0), f(0.0, torch.float64)
+    a = (z, ids, torch.zeros(N, 1, device="cuda"), None, f(1.0))
+    sv.spec_distill_forward(*a, loss, lse)
+    sv.spec_distill_backward(*a, lse, f(1.0), grad)
+    torch.cuda.synchronize()
+    e = 2.0 ** -23 * (math.log(V) + 6)
+    want = math.log(V // 2 * (1 + math.e))
+    assert (lse - want).abs().max().item() <= e
+    assert (loss - (want - 1)).abs().max().item() <= e + 2.0 ** -24 * 20
+    for n in range(N):
+        assert abs(grad[n, V - 1].item() - (math.exp(1 - want) - 1)) <= 2.0 ** -8
+        for part, q in ((grad[n, :V // 2], math.exp(-want)), (grad[n, V // 2:V - 1], math.exp(1 - want))):
+            assert abs(part.max().item() - q) <= q * 2.0 ** -7 and abs(part.min().item() - q) <= q * 2.0 ** -7
+
+
+def test_reordering_into_another_array_past_32_bit_offsets():
+    """States that start more than 2^32 bytes behind the first, in both arrays."""
+    L, B, W, K, S = 3, 2, 4, 5, 1 << 28
+    print("\n[reorder 3 x 2 x (4 -> 5) states of 256 MiB]", flush=True)
+    src = torch.empty(L, B, W, S // 4, dtype=torch.int32, device="cuda")
+    for i, state in enumerate(src.view(L * B * W, S // 4)):
+        state.copy_(torch.arange(S // 4, dtype=torch.int32, device="cuda")).mul_(i + 1)
+    dst = torch.full((L, B, K, S // 4), -1, dtype=torch.int32, device="cuda")
+    parent = torch.tensor([[3, 0, 0, -1, 2], [1, 3, 7, 2, 1]], dtype=torch.int32, device="cuda")
+    sv.spec_beam_reorder(parent, src, dst)
+    torch.cuda.synchronize()
+    for l in range(L):
+        for b in range(B):
+            for j, w in enumerate(parent[b].tolist()):
+                if 0 <= w < W:
+                    assert torch.equal(dst[l, b, j], src[l, b, w]), (l, b, j)
+                else:
+                    assert (dst[l, b, j] == -1).all(), (l, b, j)
