@@ -329,6 +329,13 @@ __device__ inline GradScale grad_scale(float weight, const RowList& l, double ls
     return g;
 }
 
+// The dense part's coefficient stays inside binary32, before it is formed (which
+// takes registers that this does not). The same in every thread, and made so.
+__device__ inline bool coef_in_reach(float weight, const RowList& l) {
+    const bool in = fabsf(weight * l.inv_t) * static_cast<float>(l.mass) <= 1e38f;
+    return __builtin_amdgcn_readfirstlane(in) != 0;
+}
+
 template <int DT>
 __device__ __forceinline__ void grad_group(const RowGroups<DT>& r, char* out, int g, bool whole,
                                            const uint4& q, float inv_t, const GradScale& c) {
@@ -418,8 +425,9 @@ __device__ inline double over_workgroup(double v, double* lds) {
 }
 
 // A row whose largest scaled logit M lies so far out (a row masked with a large
-// finite constant) that M log2e has no digits left for the sum: everything is
-// taken against M itself, and M and log S = log sum exp(x - M) stay apart,
+// finite constant) that M log2e has no digits left for the sum, or whose weight *
+// P / T is past binary32: everything is taken against M itself, and M and
+// log S = log sum exp(x - M) stay apart,
 //   q_v = exp(x_v - M) / S, loss = sum_j p_j (log p_j - (x_j - M)) + P log S,
 // one element at a time, by one workgroup, from memory: such rows are rare. Every
 // thread of the workgroup calls this, after reduce_list and before anything of the
@@ -561,14 +569,15 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
         return;
     }
     const double lse2 = lse * static_cast<double>(kLog2e);
+    const GradScale c = grad_scale(a.weight[row], l, lse2);
     // The normaliser has lost its logarithm of the sum, or soon will have: formed
-    // again, by one workgroup for the whole row (which may be its own gradient).
-    if (!(fabs(lse2) <= static_cast<double>(kReach))) {
+    // again, by one workgroup for the whole row (which may be its own gradient). So
+    // is a row whose coefficient binary32 does not hold.
+    if (!(fabs(lse2) <= static_cast<double>(kReach)) || !is_finite_f32(c.dense)) {
         if (part == 0)
             far_row<DT, THREADS, false, true>(a, row, r, l, mine, list, lds, out);
         return;
     }
-    const GradScale c = grad_scale(a.weight[row], l, lse2);
     for (int g = g0;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -612,6 +621,7 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     char* out = grad_row<DT>(a, row, r, &whole);
     Entry mine;
     const ListFetch f = fetch_list(a, row, mine);
+    const float weight = a.weight[row];
     gather<DT>(a, r, mine);
     uint4 q[R];
     r.template load<R, THREADS, true>(0, tid, r.groups, q);
@@ -636,7 +646,8 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
     const RowSum w = join<THREADS / 64>(ref, s, lds);
     const double lse2 = w.top + log2(w.sum);
     const double lse = lse2 / static_cast<double>(kLog2e);
-    const bool none = l.empty || l.bad, far = !none && !in_reach(w);
+    const bool none = l.empty || l.bad;
+    const bool far = !none && (!in_reach(w) || !coef_in_reach(weight, l));
     if (tid == 0 && !far) {
         a.out_loss[row] = l.empty ? 0.0f : l.bad ? nan : static_cast<float>(l.inner + l.mass * lse);
         a.out_lse[row] = none ? static_cast<double>(nan) : lse;
@@ -648,7 +659,7 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
             fill<DT, THREADS>(r, out, 0, r.groups, whole, l.empty ? 0.0f : nan);
         return;
     }
-    const GradScale c = grad_scale(a.weight[row], l, lse2);
+    const GradScale c = grad_scale(weight, l, lse2);
     // Steps that lie wholly inside the row go out as 16-byte stores from
     // registers; the others, at the row's ends (or of a gradient that is
     // aligned otherwise than its row), are read again.

@@ -48,6 +48,8 @@
  * workgroup several passes over the row. So large an lse no longer holds the
  * logarithm of the sum to the bound above, or at all: the backward call takes
  * from it only that the row is far, and forms the sum again from the logits.
+ * Rows whose weight * P / T is past binary32's largest value take that way too
+ * (entries that are finite then stay so).
  *
  * Layouts: dense row-major DEVICE arrays owned by the caller: logits, grad
  * [N, V] (SPEC_BF16 or SPEC_F32, aligned to the element, any V), ids [N, K]

@@ -186,3 +186,48 @@ def test_far_rows_replayed_from_a_graph():
         want = call(d, 2, False)
         got = (loss.cpu().numpy(), lse.cpu().numpy(), grad.float().cpu().numpy())
         assert all(np.array_equal(x, y, equal_nan=True) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 999, 20011, 300007])
+def test_coefficients_past_the_largest_value(V, dtype):
+    """weight / T (or P, of a teacher normaliser far too small) beyond binary32: entries of the gradient
+    whose value is inside it have that value, masked ones are 0, the others infinite. Tolerances as
+    above, with |x - lse| at most |x - M| + ln V; an exponential below 2^-120 may become zero before
+    the coefficient multiplies it."""
+    N = 6
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(N, V, generator=g)
+    z[:, V - 2:] = -math.inf                              # masked
+    T = torch.tensor([1e-36, 1e-36, 1.0, 1.0, 0.5, 2.0])
+    z[:2] = torch.where(torch.isinf(z[:2]), z[:2], 1e-36)  # x = 1 throughout
+    d = dict(logits=z.to(DTYPE[dtype]).cuda(), ids=torch.zeros(N, K, dtype=torch.int32).cuda() - 1,
+             teacher=torch.zeros(N, K).cuda(), temperature=T.cuda(),
+             weight=torch.tensor([1e3, -2e4, 1.0, -3.0, 3e38, -3e38]).cuda(),
+             teacher_lse=torch.tensor([1.0, 1.0, -100.0, -95.0, 0.0, 0.0], dtype=torch.float64).cuda())
+    d["ids"][:, 0] = 1
+    largest, half = torch.finfo(DTYPE[dtype]).max, torch.finfo(DTYPE[dtype]).eps / 2
+    zf, r = d["logits"].float().cpu().numpy(), np.float32(1) / T.numpy()
+    e = 2.0 ** -23 * (math.log(V) + 6)
+    for calls in (1, 2):
+        got = call(d, calls, False)
+        placed = call(d, calls, True)
+        assert all(np.array_equal(a, b, equal_nan=True) for a, b in zip(got, placed))
+        for n in range(N):
+            x = (zf[n] * r[n]).astype(np.float64)
+            M = x.max()
+            q = np.exp(x - M) / np.exp(x - M).sum()
+            p = math.exp(0.0 - d["teacher_lse"][n].item())
+            coef = float(d["weight"][n].item()) * float(r[n])
+            grad = coef * p * q
+            grad[1] = coef * (p * q[1] - p)
+            away = np.where(np.isinf(x), 0.0, np.abs(x - M) + math.log(V))
+            near = np.abs(coef * p * q) * (e + 2.0 ** -24 * (1.5 * away + 6)) + 2.0 ** -48 * abs(coef * p) * (np.arange(V) == 1)
+            inside = np.abs(grad) < 0.99 * largest
+            tol = near + (half + 2.0 ** -24) * (np.abs(grad) + near) + 2.0 ** -120 * max(1.0, abs(coef * p))
+            with np.errstate(invalid="ignore"):
+                off = np.abs(got[2][n] - grad)
+            assert (off[inside] <= tol[inside]).all(), (n, calls, int(np.argmax(np.where(inside, off - tol, -1))))
+            assert (got[2][n, V - 2:] == 0).all()
+            beyond = np.abs(grad) > 1.01 * largest
+            assert (np.isinf(got[2][n][beyond]) & (np.sign(got[2][n][beyond]) == np.sign(grad[beyond]))).all()
