@@ -178,7 +178,7 @@ __device__ inline RowList reduce_list(const DistillArgs& a, const ListFetch& f, 
 // All of that holds while the reference, a rounded x log2e, is within a fraction
 // of the product: within 2^-2 below 2^22. References start at -2^22 or above, so
 // that what lies below adds nothing, and a row whose own largest entry lies
-// outside (its sum then misses in_reach) is summed by far_row instead.
+// outside (in_reach) is summed by far_row instead.
 constexpr float kLazy = 256.0f;
 constexpr float kReach = 4194304.0f;
 
@@ -229,23 +229,11 @@ __device__ __forceinline__ float first_reference(const uint4& q, float inv_t) {
     return fmaxf(-kReach, scale_logit(wave_max(group_max<DT>(q)), inv_t) * kLog2e);
 }
 
-// A row's sum against its largest reference: lse * log2e = top + log2(sum).
-struct RowSum {
-    double top, sum;
-};
-
-// The row's largest entry set the reference (its term is then within 2^-2 of 1
-// in the exponent) or lies at most 2^8 above the least one. A NaN fails.
-// The same in every thread, and made so for the compiler: a branch of single lanes
-// would keep the row's registers alive over far_row.
-__device__ inline bool in_reach(const RowSum& r) {
-    const bool in = r.top <= static_cast<double>(kReach) && r.sum >= 0.25 && is_finite_f64(r.sum);
-    return __builtin_amdgcn_readfirstlane(in) != 0;
-}
-
-// The row's sum from the threads' pairs. lds: 2 values per wavefront.
+// The threads' pairs joined in two steps, lds holding a (reference, sum) for each
+// wavefront in between: what a row's end looks at decides how much of the second
+// step each wavefront does.
 template <int WAVES>
-__device__ inline RowSum join(float ref, double s, double* lds) {
+__device__ inline void join_waves(float ref, double s, double* lds) {
     const float m = wave_max(ref);
     s = wave_sum(s * static_cast<double>(ref == m ? 1.0f : fast_exp2(ref - m)));
     if ((threadIdx.x & 63) == 0) {
@@ -253,6 +241,33 @@ __device__ inline RowSum join(float ref, double s, double* lds) {
         lds[2 * (threadIdx.x >> 6) + 1] = s;
     }
     lds_barrier();
+}
+
+// Whether the sums hold, before they are joined: a reference above the least one
+// is an entry of its own wavefront, whose term is then within 2^-2 of 1 in the
+// exponent; where all are the least one, a sum says whether entries lie close
+// enough. A NaN fails. For a pass that needs the row's sum in one thread: with the
+// sum itself in a condition of the workgroup all 16 wavefronts would form it (0.5 us
+// of a row of 20011 floats).
+template <int WAVES>
+__device__ inline bool in_reach(const double* lds) {
+    const double* pair = lds + 2 * (threadIdx.x % WAVES);
+    const bool fits = pair[0] <= static_cast<double>(kReach) && is_finite_f64(pair[1]);
+    const bool some = pair[0] > -static_cast<double>(kReach) || pair[1] >= 0.25;
+    return __ballot(!fits) == 0 && __ballot(some) != 0;
+}
+
+// The same of the joined sum: nothing but a reference in reach with a sum of at
+// least its own term gives such a value. The same in every thread, and made so for
+// the compiler: a branch of single lanes would keep the row's registers alive over
+// far_row.
+__device__ inline bool lse_in_reach(double lse2) {
+    return __builtin_amdgcn_readfirstlane(fabs(lse2) <= static_cast<double>(kReach)) != 0;
+}
+
+// lse * log2e of the row.
+template <int WAVES>
+__device__ inline double join(const double* lds) {
     double top = lds[0];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w)
@@ -263,7 +278,7 @@ __device__ inline RowSum join(float ref, double s, double* lds) {
         const float d = static_cast<float>(lds[2 * w] - top);
         sum += lds[2 * w + 1] * static_cast<double>(fast_exp2(d));
     }
-    return RowSum{top, sum};
+    return top + log2(sum);
 }
 
 // ------------------------------------------------------------ the gradient ---
@@ -528,12 +543,12 @@ __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a)
             break;
         r.template load<U, THREADS>(g0, tid, r.groups, q);
     }
-    const RowSum w = join<THREADS / 64>(ref, s, lds);
-    if (!in_reach(w)) {
+    join_waves<THREADS / 64>(ref, s, lds);
+    if (!in_reach<THREADS / 64>(lds)) {
         far_row<DT, THREADS, true, false>(a, row, r, l, mine, list, lds, nullptr);
         return;
     }
-    const double lse = (w.top + log2(w.sum)) / static_cast<double>(kLog2e);
+    const double lse = join<THREADS / 64>(lds) / static_cast<double>(kLog2e);
     if (tid == 0) {
         a.out_loss[row] = static_cast<float>(l.inner + l.mass * lse);
         a.out_lse[row] = lse;
@@ -560,6 +575,7 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
     Entry mine;
     const ListFetch f = fetch_list(a, row, mine);
     const double lse = a.lse_in[row];
+    const float weight = a.weight[row];
     gather<DT>(a, r, mine);
     uint4 q[U];
     r.template load<U, THREADS>(g0, tid, g1, q);
@@ -569,11 +585,11 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
         return;
     }
     const double lse2 = lse * static_cast<double>(kLog2e);
-    const GradScale c = grad_scale(a.weight[row], l, lse2);
+    const GradScale c = grad_scale(weight, l, lse2);
     // The normaliser has lost its logarithm of the sum, or soon will have: formed
     // again, by one workgroup for the whole row (which may be its own gradient). So
     // is a row whose coefficient binary32 does not hold.
-    if (!(fabs(lse2) <= static_cast<double>(kReach)) || !is_finite_f32(c.dense)) {
+    if (!lse_in_reach(lse2) || !is_finite_f32(c.dense)) {
         if (part == 0)
             far_row<DT, THREADS, false, true>(a, row, r, l, mine, list, lds, out);
         return;
@@ -643,11 +659,11 @@ __global__ __launch_bounds__(THREADS) void distill_loss_grad_kernel(DistillArgs 
                     online_add<DT>(t[u], l.inv_t, ref, s);
             }
     }
-    const RowSum w = join<THREADS / 64>(ref, s, lds);
-    const double lse2 = w.top + log2(w.sum);
+    join_waves<THREADS / 64>(ref, s, lds);
+    const double lse2 = join<THREADS / 64>(lds);
     const double lse = lse2 / static_cast<double>(kLog2e);
     const bool none = l.empty || l.bad;
-    const bool far = !none && (!in_reach(w) || !coef_in_reach(weight, l));
+    const bool far = !none && (!lse_in_reach(lse2) || !coef_in_reach(weight, l));
     if (tid == 0 && !far) {
         a.out_loss[row] = l.empty ? 0.0f : l.bad ? nan : static_cast<float>(l.inner + l.mass * lse);
         a.out_lse[row] = none ? static_cast<double>(nan) : lse;
