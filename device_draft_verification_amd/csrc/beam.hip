@@ -169,7 +169,9 @@ __device__ __forceinline__ void repack(uint4 (&q)[U]) {
 // enough workgroups per CU to load while others select. Bound by the read of the
 // logits (256 x 8 beams of 152064 bf16, K = 8: 83 us, 7.5 TB/s, part of it from the
 // last-level cache; 4 groups 99 us, 12 90 us; 64 x 16 beams of 128256, K = 32: 38
-// us, 6.8 TB/s). Small calls are a chain of latencies (4 beams of 32000 floats: 6 us).
+// us, 6.8 TB/s). Forming the normalisers takes an exponential for each entry beside
+// that: 120 and 56 us. Small calls are a chain of latencies (4 beams of 32000 floats:
+// 6 us).
 template <int DT, int T, int U, bool NORM>
 __global__ __launch_bounds__(T) void beam_piece_kernel(
     const void* __restrict__ logits, const float* __restrict__ score,
@@ -377,7 +379,8 @@ constexpr double kFarNormaliser = 4194304.0;
 // the keys are few (16 beams x 8 pieces x 32 of 64 sequences: 2 MB beside the logits' 263),
 // so its time is the latency of its steps (read, histogram, collect, rank): 5.7 us
 // for one sequence, 6.6 us for 256 of 8 beams and K = 8, 11.3 us for the 4096 keys
-// above. Up to 4096 keys stay in registers over the steps.
+// above. Up to 4096 keys stay in registers over the steps; more are read again in
+// each (40960 of 64 beams, K = 64: 65 us, more than their pieces' 58).
 template <bool NORM>
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(
     const float* score /* may be out_score */, const double* __restrict__ lse, int beams, int keep,
@@ -597,7 +600,9 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 // In place: one thread owns one T-sized column of every slot of a (layer,
 // sequence), at most NB, and reads the parents' columns before it writes any
 // slot, so that a permutation needs no other order. Reads and writes each moved
-// slot once; small states are one latency (4 layers x 4 beams of 16 KiB: 3 us).
+// slot once; small states are one latency (4 layers x 4 beams of 16 KiB: 3 us), large
+// ones move at 5.8-6.0 TB/s of what is moved (8 layers x 32 sequences x 8 beams of 512
+// KiB, 1.67 GB: 284 us; 4 x 16 x 64 beams of 256 KiB, 2.07 GB: 355).
 template <typename T, int NB>
 __global__ __launch_bounds__(kBlock) void beam_reorder_kernel(long states, int batch, int beams,
                                                               const int32_t* __restrict__ parent,

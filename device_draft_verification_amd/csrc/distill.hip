@@ -444,9 +444,10 @@ __device__ inline double over_workgroup(double v, double* lds) {
 // P / T is past binary32: everything is taken against M itself, and M and
 // log S = log sum exp(x - M) stay apart,
 //   q_v = exp(x_v - M) / S, loss = sum_j p_j (log p_j - (x_j - M)) + P log S,
-// one element at a time, by one workgroup, from memory: such rows are rare. Every
-// thread of the workgroup calls this, after reduce_list and before anything of the
-// row's gradient is written.
+// one element at a time, by one workgroup, from memory: such rows are rare (128256
+// bf16: one row 52 us forward, 126 in one call; 640 rows 260 and 840). Every thread of
+// the workgroup calls this, after reduce_list and before anything of the row's
+// gradient is written.
 template <int DT, int THREADS, bool LOSS, bool GRAD>
 __device__ inline void far_row(const DistillArgs& a, long row, const RowGroups<DT>& r, const RowList& l,
                                const Entry& mine, const ListLds& list, double* lds, char* out) {
@@ -509,7 +510,8 @@ __device__ inline void far_row(const DistillArgs& a, long row, const RowGroups<D
 // 33 us, 4.9 TB/s, 2.5 rows per CU). Few rows take 1024 threads each, for more loads
 // in flight; many take 512, so that one row's reductions hide behind another's
 // loads (1024 threads, 256, or 8 groups per thread at a time cost 8 to 16 us
-// more). 37 rows of 20011 floats: 7.7 us, latency.
+// more). 37 rows of 20011 floats: 7.7 us, latency. A row is one workgroup's however
+// few there are: 1 to 128 rows of 152064 bf16 take 14 to 17 us.
 template <int DT, int THREADS, int U>
 __global__ __launch_bounds__(THREADS) void distill_forward_kernel(DistillArgs a) {
     using Row = RowGroups<DT>;
@@ -614,11 +616,16 @@ __global__ __launch_bounds__(THREADS) void distill_backward_kernel(DistillArgs a
 
 // The row's first R * THREADS groups stay in registers; those behind them
 // (TAIL), kTailUnroll per thread at a time, are read again for the gradient.
-// 2304 rows of 152064 bf16 (1.4 GB read and written): 335-350 us, 4.0-4.2 TB/s; a
+// 2304 rows of 152064 bf16 (1.4 GB read and written): 340-355 us, 4.0-4.1 TB/s; a
 // copy with one workgroup per row takes 267 us, one along a single front 217, and
-// the two passes apart 454. What is left over the copy is a row's own order: its
-// first gradient waits for its last logit, and a row of 304 KB in registers leaves
-// room for no second workgroup on the CU that would cover for the wait. (Workgroups
+// the two passes above, which read the row twice, 345 (110 and 235; in chunks of 420
+// rows, whose second read may come from the last-level cache, 445). What is left over
+// the copy is a row's own order: its first gradient waits for its last logit, and
+// with 304 KB of a CU's 512 KB of registers in one row there is no second workgroup
+// to cover for the wait; the 160 KB of LDS hold no part of a row so far. 1024 rows
+// of 128256 floats, 40 % of each read again: 260 us, the two passes 258. Few long
+// rows are one workgroup each: 1 to 64 rows of 152064 bf16 32-35 us, where the two
+// passes, the second of them split, take 24-30. (Workgroups
 // that stay for several rows and load the next row's groups as the gradients free
 // their registers: 339-381 us; 16 groups in registers and the rest read again, which
 // fits twice on a CU: 390; 20 groups so: 385; 1024 threads of 10 and the rest read
@@ -725,7 +732,9 @@ void launch_backward(int rows, const DistillArgs& a, hipStream_t s) {
 
 template <int DT>
 void launch_loss_grad(int rows, const DistillArgs& a, hipStream_t s) {
-    // at any alignment of the row's start
+    // The smallest size that holds the row; the largest is what the registers hold
+    // (38 groups take 152 of a thread's 256, beside about 48 others), the others leave
+    // room for more workgroups on the CU. At any alignment of the row's start:
     const long groups = (static_cast<long>(a.vocab) + RowGroups<DT>::W - 1) / RowGroups<DT>::W + 1;
 #define SPEC_RESIDENT(T, R)                                                                \
     if (groups <= (T) * (R)) {                                                             \
