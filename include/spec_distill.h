@@ -56,7 +56,7 @@
  * int32, teacher [N, K] float32, teacher_lse [N] float64 or NULL, temperature,
  * weight, loss [N] float32, lse [N] float64. grad may be the logits array
  * itself (the gradient then takes its place); no other overlap. 1 <= K <=
- * SPEC_DISTILL_MAX_K, V >= 1, N >= 0.
+ * SPEC_DISTILL_MAX_K, V >= 1, 0 <= N < 2^22 (one dispatch).
  *
  * Asynchrony and errors: as in spec_verify.h; each call enqueues one kernel on
  * hip_stream (a hipStream_t, NULL = the null stream), needs no workspace, and

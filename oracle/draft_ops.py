@@ -12,13 +12,19 @@ from __future__ import annotations
 import numpy as np
 
 
-def row_lse(x):
-    """log sum exp over the last axis, float64."""
+def row_parts(x):
+    """The largest entry M of the last axis (0 where it is not finite) and log sum exp(x - M)."""
     x = np.asarray(x, np.float64)
     with np.errstate(invalid="ignore", divide="ignore"):
         m = x.max(-1, keepdims=True)
         safe = np.where(np.isfinite(m), m, 0.0)
-        return (safe + np.log(np.exp(x - safe).sum(-1, keepdims=True)))[..., 0]
+        return safe[..., 0], np.log(np.exp(x - safe).sum(-1, keepdims=True))[..., 0]
+
+
+def row_lse(x):
+    """log sum exp over the last axis, float64."""
+    m, log_s = row_parts(x)
+    return m + log_s
 
 
 def beam_select(logits, score, lse, keep):
@@ -26,8 +32,12 @@ def beam_select(logits, score, lse, keep):
     Returns parent, token [B, K] int32 and value, logq [B, K] float64."""
     z = np.asarray(logits, np.float32)
     B, W, V = z.shape
+    top = np.zeros((B, W))
     if lse is None:
         lse = row_lse(z)
+        m, log_s = row_parts(z)
+        far = np.isfinite(lse) & (np.abs(lse) > 2.0 ** 22)
+        top, lse = np.where(far, m, 0.0), np.where(far, log_s, lse)
     parent = np.full((B, keep), -1, np.int32)
     token = np.full((B, keep), -1, np.int32)
     value = np.full((B, keep), -np.inf)
@@ -36,7 +46,7 @@ def beam_select(logits, score, lse, keep):
         alive = np.isfinite(score[b]) & np.isfinite(lse[b])
         ok = np.isfinite(z[b]) & alive[:, None]
         w, v = np.nonzero(ok)
-        q = z[b, w, v].astype(np.float64) - lse[b, w]
+        q = (z[b, w, v].astype(np.float64) - top[b, w]) - lse[b, w]
         val = score[b, w].astype(np.float64) + q
         order = np.lexsort((v, -z[b, w, v], w, -val))[:keep]
         n = order.size
@@ -63,6 +73,7 @@ def distill_scaled(x, ids, y, teacher_lse, weight, r):
     x = np.asarray(x, np.float64)
     N, V = x.shape
     lse = row_lse(x)
+    top, log_s = row_parts(x)
     loss, grad = np.zeros(N), np.zeros((N, V))
     for n in range(N):
         j = np.nonzero(ids[n] >= 0)[0]
@@ -73,9 +84,9 @@ def distill_scaled(x, ids, y, teacher_lse, weight, r):
         logp = y[n, j].astype(np.float64) - lt
         p = np.exp(logp)
         with np.errstate(invalid="ignore"):
-            terms = np.where(p > 0, p * (logp - (x[n, ids[n, j]] - lse[n])), 0.0)
+            terms = np.where(p > 0, p * (logp - ((x[n, ids[n, j]] - top[n]) - log_s[n])), 0.0)
         loss[n] = terms.sum()
-        g = p.sum() * np.exp(x[n] - lse[n])
+        g = p.sum() * np.exp((x[n] - top[n]) - log_s[n])
         np.add.at(g, ids[n, j], -p)
         grad[n] = weight[n] * r[n] * g
     return loss, lse, grad
