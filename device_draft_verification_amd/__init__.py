@@ -6,8 +6,10 @@ C ABI of ``include/spec_verify.h`` (verification), ``include/spec_bandit.h``
 its fused normaliser), ``include/spec_tree.h`` (draft-tree pruning and
 greedy tree verification), ``include/spec_beam.h`` (beam selection and the
 reordering of the beams' states), ``include/spec_distill.h`` (distillation from
-a teacher's top logits) and ``include/spec_int8.h`` (row quantisation and the
-8-bit integer product); this package is a thin ctypes binding with
+a teacher's top logits), ``include/spec_int8.h`` (row quantisation and the
+8-bit integer product), ``include/spec_mxfp4.h`` (the same in 4-bit floating
+point with block scales) and ``include/spec_logprobs.h`` (scores of given tokens
+and their gradient); this package is a thin ctypes binding with
 the same function names (``binding``) and the build script (``build``).
 """
 from .binding import (  # noqa: F401
@@ -30,4 +32,7 @@ from .binding import (  # noqa: F401
     spec_beam_select, spec_beam_set_stream,
     SPEC_DISTILL_MAX_K, spec_distill_backward, spec_distill_forward, spec_distill_loss_grad,
     SPEC_INT8_MAX_DEPTH, spec_int8_product, spec_quantize_rows,
+    SPEC_MXFP4_MAX_DEPTH, spec_mxfp4_padded, spec_mxfp4_product, spec_mxfp4_quantize_rows,
+    SPEC_LOGPROBS_MAX_K, LogprobsContext, spec_logprobs_destroy, spec_logprobs_init,
+    spec_logprobs_set_stream, spec_token_logprobs, spec_token_logprobs_backward,
 )

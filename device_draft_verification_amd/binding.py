@@ -46,11 +46,16 @@ EXPORTED = (
     "spec_beam_reorder",
     "spec_distill_forward", "spec_distill_backward", "spec_distill_loss_grad",
     "spec_quantize_rows", "spec_int8_product",
+    "spec_mxfp4_quantize_rows", "spec_mxfp4_product",
+    "spec_logprobs_init", "spec_logprobs_set_stream", "spec_token_logprobs",
+    "spec_token_logprobs_backward", "spec_logprobs_destroy",
 )
 
 SPEC_BEAM_MAX = 64
 SPEC_DISTILL_MAX_K = 256
 SPEC_INT8_MAX_DEPTH = 131056
+SPEC_MXFP4_MAX_DEPTH = 1 << 20
+SPEC_LOGPROBS_MAX_K = 64
 
 SPEC_TREE_MAX_NODES = 256
 
@@ -126,6 +131,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_distill_loss_grad": ([i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P], i32),
         "spec_quantize_rows": ([i32, i32, i32, P, P, P, P], i32),
         "spec_int8_product": ([i32, i32, i32, P, P, P, P, i32, P, P], i32),
+        "spec_mxfp4_quantize_rows": ([i32, i32, i32, P, P, P, P, P], i32),
+        "spec_mxfp4_product": ([i32, i32, i32, P, P, P, P, i32, P, P], i32),
+        "spec_logprobs_init": ([i32, i32, i32, i32, P, ctypes.POINTER(P)], i32),
+        "spec_logprobs_set_stream": ([P, P], i32),
+        "spec_token_logprobs": ([P, i32, P, P, P, P, P, P, P, P, P], i32),
+        "spec_token_logprobs_backward": ([P, i32, P, P, P, P, P, P, P, P], i32),
+        "spec_logprobs_destroy": ([P], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -812,3 +824,132 @@ def spec_int8_product(a, a_scale, w, w_scale, out, stream=None) -> None:
             _arg(a_scale, (N,), f32, "a_scale", dev), _arg(w, (V, D), i8, "w", dev),
             _arg(w_scale, (V,), f32, "w_scale", dev), dtype_code(out.dtype),
             _arg(out, (N, V), out.dtype, "out", dev))
+
+
+def spec_mxfp4_padded(cols: int) -> int:
+    """The entries that rows of `cols` entries are padded to in 4 bits: whole groups of 128."""
+    return (cols + 127) // 128 * 128
+
+
+def spec_mxfp4_quantize_rows(x, out_q, out_scale, out_values=None, stream=None) -> None:
+    """x [N, D] float32 or bfloat16 to 4-bit floating point with a scale for every 32 entries;
+    with D' = spec_mxfp4_padded(D): out_q [N, D' / 2] uint8 (two codes each), out_scale
+    [N, D' / 32] uint8 (exponents plus 127), out_values [N, D] in x's dtype (what the codes
+    stand for; may be x itself) or None."""
+    if x.dim() != 2:
+        raise ValueError("x is [N, D]")
+    shape, dev = x.shape, x.get_device()
+    N, D = shape
+    whole = spec_mxfp4_padded(D)
+    _launch("spec_mxfp4_quantize_rows", dev, stream, N, D, dtype_code(x.dtype),
+            _arg(x, shape, x.dtype, "x", dev), _arg(out_q, (N, whole // 2), torch.uint8, "out_q", dev),
+            _arg(out_scale, (N, whole // 32), torch.uint8, "out_scale", dev),
+            _arg(out_values, shape, x.dtype, "out_values", dev))
+
+
+def spec_mxfp4_product(a, a_scale, w, w_scale, out, stream=None) -> None:
+    """out[n, v] = sum_k of a's and w's values over their scaled 4-bit codes: a [N, D' / 2] and
+    w [V, D' / 2] uint8 with scales [N, D' / 32] and [V, D' / 32] uint8 as
+    spec_mxfp4_quantize_rows leaves them, out [N, V] float32 or bfloat16."""
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a is [N, D' / 2], w is [V, D' / 2]")
+    (N, half), V, dev = a.shape, w.shape[0], a.get_device()
+    u8 = torch.uint8
+    _launch("spec_mxfp4_product", dev, stream, N, 2 * half, V, _arg(a, (N, half), u8, "a", dev),
+            _arg(a_scale, (N, half // 16), u8, "a_scale", dev), _arg(w, (V, half), u8, "w", dev),
+            _arg(w_scale, (V, half // 16), u8, "w_scale", dev), dtype_code(out.dtype),
+            _arg(out, (N, V), out.dtype, "out", dev))
+
+
+class LogprobsContext:
+    """Owns a spec_logprobs_ctx*; destroyed with spec_logprobs_destroy."""
+
+    def __init__(self, handle: ctypes.c_void_p, rows: int, vocab: int, top_k: int, dtype: int,
+                 device: int):
+        self.handle = handle
+        self.rows, self.vocab, self.top_k = rows, vocab, top_k
+        self.dtype, self.device = dtype, device
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            try:
+                load_library().spec_logprobs_destroy(self.handle)
+            except Exception:
+                pass
+            self.handle = None
+
+
+def spec_logprobs_init(rows: int, vocab: int, top_k: int, dtype, stream=None) -> LogprobsContext:
+    """For calls of at most `rows` rows of `vocab` logits, with lists of `top_k` alternatives (0:
+    none)."""
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    device = torch.cuda.current_device()
+    _refuse_other_device("spec_logprobs_init", device, stream)
+    h = ctypes.c_void_p()
+    _check("spec_logprobs_init", load_library().spec_logprobs_init(
+        rows, vocab, top_k, code, _stream_handle(stream), ctypes.byref(h)))
+    return LogprobsContext(h, rows, vocab, top_k, code, device)
+
+
+def spec_logprobs_set_stream(ctx: LogprobsContext, stream=None) -> None:
+    """Later calls of this context run on `stream` (None: the current one). What the earlier
+    stream still holds has to be waited for first: they share the workspace."""
+    _refuse_other_device("spec_logprobs_set_stream", ctx.device, stream)
+    _check("spec_logprobs_set_stream",
+           load_library().spec_logprobs_set_stream(ctx.handle, _stream_handle(stream)))
+
+
+def _logprobs_args(ctx, logits, token, temperature):
+    if logits.dim() != 2 or logits.shape[0] > ctx.rows:
+        raise ValueError(f"logits are [N, {ctx.vocab}] with N at most {ctx.rows}, got {tuple(logits.shape)}")
+    N, dev = logits.shape[0], ctx.device
+    dtype = torch.bfloat16 if ctx.dtype == SPEC_BF16 else torch.float32
+    return N, dev, dtype, (ctx.handle, N, _arg(logits, (N, ctx.vocab), dtype, "logits", dev),
+                           _arg(token, (N,), torch.int32, "token", dev),
+                           _arg(temperature, (N,), torch.float32, "temperature", dev))
+
+
+def spec_token_logprobs(ctx: LogprobsContext, logits, token, temperature, out_logprob, out_rank,
+                        out_entropy, out_top_token, out_top_logprob, out_norm) -> None:
+    """Scores of one token per row: logits [N, V] in the context's dtype (N at most its rows),
+    token [N] int32 (negative: none), temperature [N] float32 or None (1); out_logprob,
+    out_entropy [N] float32, out_rank [N] int32, out_top_token [N, K] int32 and out_top_logprob
+    [N, K] float32 (None when the context's top_k is 0), out_norm [N, 2] float32 (the largest
+    scaled logit and the logarithm of the sum against it). Runs on the context's stream, whatever
+    stream is current."""
+    N, dev, _, args = _logprobs_args(ctx, logits, token, temperature)
+    K, f32, i32 = ctx.top_k, torch.float32, torch.int32
+    if K and (out_top_token is None or out_top_logprob is None):
+        raise ValueError(f"lists of the {K} top alternatives expected")
+    rc = (_lib or load_library()).spec_token_logprobs(
+        *args, _arg(out_logprob, (N,), f32, "out_logprob", dev), _arg(out_rank, (N,), i32, "out_rank", dev),
+        _arg(out_entropy, (N,), f32, "out_entropy", dev),
+        _arg(out_top_token, (N, K), i32, "out_top_token", dev) if K else None,
+        _arg(out_top_logprob, (N, K), f32, "out_top_logprob", dev) if K else None,
+        _arg(out_norm, (N, 2), f32, "out_norm", dev))
+    if rc < 0:
+        raise SpecVerifyError("spec_token_logprobs", rc)
+
+
+def spec_token_logprobs_backward(ctx: LogprobsContext, logits, token, temperature, norm, entropy,
+                                 grad_logprob, grad_entropy, out_grad) -> None:
+    """Gradient of sum_n (grad_logprob[n] logprob[n] + grad_entropy[n] entropy[n]) for the
+    logits: norm [N, 2] and entropy [N] float32 from the forward call, grad_logprob [N] and
+    grad_entropy [N] (or None) float32; out_grad [N, V] in the logits' dtype (may be the logits).
+    Runs on the context's stream, whatever stream is current."""
+    N, dev, dtype, args = _logprobs_args(ctx, logits, token, temperature)
+    f32 = torch.float32
+    rc = (_lib or load_library()).spec_token_logprobs_backward(
+        *args, _arg(norm, (N, 2), f32, "norm", dev), _arg(entropy, (N,), f32, "entropy", dev),
+        _arg(grad_logprob, (N,), f32, "grad_logprob", dev),
+        _arg(grad_entropy, (N,), f32, "grad_entropy", dev),
+        _arg(out_grad, logits.shape, dtype, "out_grad", dev))
+    if rc < 0:
+        raise SpecVerifyError("spec_token_logprobs_backward", rc)
+
+
+def spec_logprobs_destroy(ctx: LogprobsContext) -> None:
+    if ctx.handle:
+        rc = load_library().spec_logprobs_destroy(ctx.handle)
+        ctx.handle = None
+        _check("spec_logprobs_destroy", rc)

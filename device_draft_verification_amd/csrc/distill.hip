@@ -22,6 +22,7 @@
 #include "launch.hpp"
 #include "rows.hpp"
 #include "spec_distill.h"
+#include "stage.hpp"
 
 namespace specv {
 namespace {
@@ -65,17 +66,6 @@ struct ListLds {
     int flags[4];
     double sum[4], inner[4];
 };
-
-// The workgroup's barrier for exchanges through LDS: unlike __syncthreads it
-// does not wait for global loads, so that a row stays on its way while its list
-// is reduced. The empty asm keeps the compiler from moving accesses across.
-__device__ __forceinline__ void lds_barrier() {
-    asm volatile("" ::: "memory");
-    // s_waitcnt: lgkmcnt 0, vmcnt and expcnt at their largest (not waited)
-    __builtin_amdgcn_s_waitcnt((0xF) | (0x3 << 14) | (0x7 << 4));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 struct ListFetch {
     float t;      // the row's temperature
@@ -283,51 +273,6 @@ __device__ inline double join(const double* lds) {
 
 // ------------------------------------------------------------ the gradient ---
 
-template <int DT>
-__device__ inline void store_element(void* row, long v, float g) {
-    if constexpr (DT == kBF16) {
-        const __bf16 h = static_cast<__bf16>(g);
-        reinterpret_cast<__bf16*>(row)[v] = h;
-    } else {
-        reinterpret_cast<float*>(row)[v] = g;
-    }
-}
-
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-template <int DT>
-__device__ __forceinline__ u32x4 pack_group(const float (&d)[RowGroups<DT>::W]) {
-    u32x4 v;
-    if constexpr (DT == kBF16) {
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{d[2 * i], d[2 * i + 1]}, bf16x2));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = __float_as_uint(d[i]);
-    }
-    return v;
-}
-
-// Group g of the row's gradient; `whole`: it can go out as one 16-byte store.
-template <int DT>
-__device__ inline void store_group(const RowGroups<DT>& r, char* out, int g, bool whole,
-                                   const float (&d)[RowGroups<DT>::W]) {
-    constexpr int W = RowGroups<DT>::W;
-    const long e0 = r.element(g);
-    if (whole && r.inside(g)) {
-        __builtin_nontemporal_store(pack_group<DT>(d), reinterpret_cast<u32x4*>(out + e0 * RowGroups<DT>::ESZ));
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-        if (e0 + i >= 0 && e0 + i < r.vocab)
-            store_element<DT>(out, e0 + i, d[i]);
-}
-
 // The row's coefficients: exp(x - lse) = 2^(x log2e - ref) * 2^(ref - lse log2e),
 // the second factor (within 2^-2 in the exponent below kReach) taken into the
 // coefficient.
@@ -374,16 +319,6 @@ __device__ __forceinline__ void grad_group_inside(const RowGroups<DT>& r, char* 
     for (int e = 0; e < W; ++e)
         d[e] = c.dense * fast_exp2(__builtin_fmaf(scale_logit(z[e], inv_t), kLog2e, -c.ref));
     reinterpret_cast<u32x4*>(out - r.shift * RowGroups<DT>::ESZ)[g] = pack_group<DT>(d);
-}
-
-template <int DT, int THREADS>
-__device__ inline void fill(const RowGroups<DT>& r, char* out, int g0, int g1, bool whole, float v) {
-    float d[RowGroups<DT>::W];
-#pragma unroll
-    for (int e = 0; e < RowGroups<DT>::W; ++e)
-        d[e] = v;
-    for (int g = g0 + static_cast<int>(threadIdx.x); g < g1; g += THREADS)
-        store_group<DT>(r, out, g, whole, d);
 }
 
 // The listed places, after the dense part: the first entry of an id writes the

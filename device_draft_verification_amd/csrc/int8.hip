@@ -9,6 +9,7 @@
 
 #include "rows.hpp"
 #include "spec_int8.h"
+#include "stage.hpp"
 
 namespace specv {
 namespace {
@@ -215,22 +216,6 @@ hipError_t launch_quantize(int rows, int cols, const void* x, int8_t* out_q, flo
 // 1641). Few rows are bound by the read of the weights: 1 row x 152064,
 // D = 4096 127 us, 64 rows at D = 512 19 us, 5 TB/s each.
 __device__ int4 zero_chunk;  // zero from load on, never written
-
-__device__ constexpr int wait_loads(int n) {
-    // s_waitcnt operand: vmcnt n (bits 3:0 and 15:14), lgkmcnt 0 (bits 11:8), expcnt not waited
-    return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4);
-}
-
-// At most n global loads and no LDS access of this wavefront outstanding, then
-// the workgroup's barrier. Unlike __syncthreads it leaves the n youngest loads
-// in flight; the empty asm keeps the compiler from moving memory accesses across.
-template <int N>
-__device__ __forceinline__ void stage_barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(wait_loads(N));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 template <int TV, int TN, int WV, int WN, int BK, int RING, int OUT>
 __global__ __launch_bounds__(64 * WV * WN, 2) void int8_product_kernel(

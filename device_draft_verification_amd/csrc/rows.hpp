@@ -183,6 +183,62 @@ struct RowGroups {
     }
 };
 
+template <int DT>
+__device__ inline void store_element(void* row, long v, float g) {
+    if constexpr (DT == kBF16) {
+        const __bf16 h = static_cast<__bf16>(g);
+        reinterpret_cast<__bf16*>(row)[v] = h;
+    } else {
+        reinterpret_cast<float*>(row)[v] = g;
+    }
+}
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ u32x4 pack_group(const float (&d)[RowGroups<DT>::W]) {
+    u32x4 v;
+    if constexpr (DT == kBF16) {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{d[2 * i], d[2 * i + 1]}, bf16x2));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __float_as_uint(d[i]);
+    }
+    return v;
+}
+
+// Group g of an output row beside the row; `whole`: it can go out as one 16-byte store.
+template <int DT>
+__device__ inline void store_group(const RowGroups<DT>& r, char* out, int g, bool whole,
+                                   const float (&d)[RowGroups<DT>::W]) {
+    constexpr int W = RowGroups<DT>::W;
+    const long e0 = r.element(g);
+    if (whole && r.inside(g)) {
+        __builtin_nontemporal_store(pack_group<DT>(d), reinterpret_cast<u32x4*>(out + e0 * RowGroups<DT>::ESZ));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        if (e0 + i >= 0 && e0 + i < r.vocab)
+            store_element<DT>(out, e0 + i, d[i]);
+}
+
+// Groups [g0, g1) of the row, all of it v.
+template <int DT, int THREADS>
+__device__ inline void fill(const RowGroups<DT>& r, char* out, int g0, int g1, bool whole, float v) {
+    float d[RowGroups<DT>::W];
+#pragma unroll
+    for (int e = 0; e < RowGroups<DT>::W; ++e)
+        d[e] = v;
+    for (int g = g0 + static_cast<int>(threadIdx.x); g < g1; g += THREADS)
+        store_group<DT>(r, out, g, whole, d);
+}
+
 __device__ inline bool is_finite_f32(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 __device__ inline bool is_finite_f64(double x) {
     return ((static_cast<uint64_t>(__double_as_longlong(x)) >> 52) & 0x7FF) != 0x7FF;

@@ -2,10 +2,13 @@
 
 Beam selection and state reordering (include/spec_beam.h), distillation from a teacher's top
 logits (include/spec_distill.h), row quantisation and the integer product (include/spec_int8.h),
-written from the definitions in those headers. Only the test suite imports this module.
+their 4-bit counterparts (include/spec_mxfp4.h), scores of given tokens and their gradient
+(include/spec_logprobs.h), written from the definitions in those headers. Only the test suite imports this module.
 Pinned in tests/test_oracle_draft_ops.py: the selection by sorting Python tuples, the loss by
 torch's log_softmax in float64, the gradient by autograd and by central differences, the
-quantisation by exact fractions, the product by Python integers.
+quantisation by exact fractions, the product by Python integers; the 4-bit forms and the scores in
+tests/test_oracle_scores.py, by a table's nearest entry, exact fractions, Python sorting, torch's
+log_softmax and autograd in float64, and central differences.
 """
 from __future__ import annotations
 
@@ -140,3 +143,138 @@ def int8_product(a, a_scale, w, w_scale):
     f = acc.astype(np.float32)
     with np.errstate(all="ignore"):
         return (f * a_scale[:, None].astype(np.float32)) * w_scale[None, :].astype(np.float32)
+
+
+MXFP4_LEVELS = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def mxfp4_quantize(x):
+    """x [N, D] float32 values: codes [N, D' / 2] uint8, scales [N, D' / 32] uint8, values
+    [N, D] float64."""
+    x = np.asarray(x, np.float32).astype(np.float64)
+    N, D = x.shape
+    whole = (D + 127) // 128 * 128
+    y = np.zeros((N, whole))
+    y[:, :D] = x
+    y = y.reshape(N, -1, 32)
+    wild = ~np.isfinite(y).all(2)
+    y = np.where(wild[..., None], 0.0, y)
+    top = np.abs(y).max(2)
+    e = np.maximum(np.frexp(top)[1] - 1 - 2, -127)
+    e = np.where(top == 0, -127, e)
+    mag = np.ldexp(np.abs(y), -e[..., None])
+    # the step of the representable values around mag; ties to even of mag / step are ties to the
+    # even code (each octave holds two codes, the even one first)
+    step = np.where(mag < 2, 0.5, np.where(mag < 4, 1.0, 2.0))
+    level = np.minimum(np.rint(mag / step) * step, 6.0)
+    code = np.searchsorted(MXFP4_LEVELS, level).astype(np.uint8)
+    code = (code + 8 * np.signbit(y)).astype(np.uint8)
+    code[wild] = 0
+    values = np.where(wild[..., None], np.nan, np.ldexp(np.copysign(level, y), e[..., None]))
+    code = code.reshape(N, whole)
+    scale = np.where(wild, 255, e + 127).astype(np.uint8)
+    return code[:, 0::2] | code[:, 1::2] << 4, scale, values.reshape(N, whole)[:, :D]
+
+
+def mxfp4_values(q, scale):
+    """What codes [N, D' / 2] with scales [N, D' / 32] stand for, float64 [N, D']."""
+    code = np.stack((q & 15, q >> 4), 2).reshape(q.shape[0], -1, 32).astype(np.int64)
+    v = MXFP4_LEVELS[code & 7] * np.where(code & 8, -1.0, 1.0)
+    v = np.ldexp(v, scale.astype(np.int64)[..., None] - 127)
+    return np.where((scale == 255)[..., None], np.nan, v).reshape(q.shape[0], -1)
+
+
+def mxfp4_product(q, scale, wq, w_scale):
+    """The exact product rounded to float64, and sum_k |a w|."""
+    a, w = mxfp4_values(q, scale), mxfp4_values(wq, w_scale)
+    with np.errstate(invalid="ignore"):
+        return a @ w.T, np.abs(a) @ np.abs(w).T
+
+
+def score_scaled(z, temperature):
+    """x [N, V] float32 = fl32(z fl32(1/T)) (NaN rows of bad temperatures) and r [N] float32."""
+    z = np.asarray(z, np.float32)
+    if temperature is None:
+        r = np.ones(z.shape[0], np.float32)
+    else:
+        t = np.asarray(temperature, np.float32)
+        with np.errstate(all="ignore"):
+            r = (np.float32(1.0) / t).astype(np.float32)
+            r = np.where((t > 0) & np.isfinite(t) & np.isfinite(r), r, np.float32(np.nan)).astype(np.float32)
+    with np.errstate(all="ignore"):
+        return (z * r[:, None]).astype(np.float32), r
+
+
+def token_scores(z, token, temperature, keep):
+    """z [N, V] float32 values, token [N], temperature [N] float32 or None. Returns a dict of
+    logprob, entropy [N], norm [N, 2], top_logprob [N, K] float64, rank [N], top_token [N, K] int32."""
+    z = np.asarray(z, np.float32)
+    x, _ = score_scaled(z, temperature)
+    N, V = z.shape
+    out = dict(logprob=np.zeros(N), rank=np.full(N, -1, np.int32), entropy=np.zeros(N),
+               norm=np.zeros((N, 2)), top_token=np.full((N, keep), -1, np.int32),
+               top_logprob=np.full((N, keep), -np.inf))
+    for n in range(N):
+        xn, t = x[n].astype(np.float64), int(token[n])
+        m = xn.max()
+        if np.isnan(xn).any() or m == np.inf:
+            for k in ("logprob", "entropy", "norm", "top_logprob"):
+                out[k][n] = np.nan
+            continue
+        if m == -np.inf:
+            out["norm"][n] = (m, 0.0)
+            out["logprob"][n] = 0.0 if t < 0 else np.nan if t >= V else -np.inf
+            continue
+        d = xn - m
+        e = np.exp(d)
+        log_s = np.log(e.sum())
+        out["norm"][n] = (m, log_s)
+        out["entropy"][n] = log_s - (e * np.where(e > 0, d, 0.0)).sum() / e.sum()
+        order = np.argsort(-z[n], kind="stable")
+        if t >= V:
+            out["logprob"][n] = np.nan
+        elif t >= 0:
+            out["logprob"][n] = d[t] - log_s
+            out["rank"][n] = np.nonzero(order == t)[0][0]
+        top = order[:keep]
+        top = top[xn[top] > -np.inf]
+        out["top_token"][n, :top.size] = top
+        out["top_logprob"][n, :top.size] = d[top] - log_s
+    return out
+
+
+def score_parts(x):
+    """log p [N, V] and entropy [N] of finite-topped rows x [N, V], float64."""
+    x = np.asarray(x, np.float64)
+    m, log_s = row_parts(x)
+    l = (x - m[:, None]) - log_s[:, None]
+    p = np.exp(l)
+    return l, p, -(p * np.where(p > 0, l, 0.0)).sum(1)
+
+
+def score_grad_scaled(x, token, a, b, r):
+    """Gradient of sum_n (a logprob + b entropy) for z with x = r z: valid rows only."""
+    l, p, h = score_parts(x)
+    a = np.where(token >= 0, a, 0.0)
+    g = -p * (a[:, None] + b[:, None] * (np.where(p > 0, l, 0.0) + h[:, None]))
+    at = np.nonzero(token >= 0)[0]
+    g[at, token[at]] += a[at]
+    return g * r[:, None]
+
+
+def token_scores_grad(z, token, temperature, a, b):
+    """The header's definition, its sentinels included: float64 [N, V]."""
+    z = np.asarray(z, np.float32)
+    N, V = z.shape
+    x, r = score_scaled(z, temperature)
+    with np.errstate(all="ignore"):
+        m = x.max(1)
+        bad = np.isnan(x).any(1) | (m == np.inf) | (token >= V) | ~np.isfinite(r)
+        empty = ~bad & (m == -np.inf)
+        safe = np.where((bad | empty)[:, None], np.float32(0), x)
+        g = score_grad_scaled(safe, np.where(token >= V, -1, token), np.asarray(a, np.float64),
+                              np.zeros(N) if b is None else np.asarray(b, np.float64),
+                              np.where(np.isfinite(r), r, 1.0).astype(np.float64))
+    g[empty] = 0.0
+    g[bad] = np.nan
+    return g
