@@ -14,6 +14,7 @@
 
 #include <cstdint>
 #include <new>
+#include <type_traits>
 
 #include "launch.hpp"
 #include "rows.hpp"
@@ -24,10 +25,9 @@
 namespace specv {
 namespace {
 
-constexpr int kT = kBlock;     // threads of a workgroup
-constexpr int kU = 4;          // 16-byte groups of a step per thread
-constexpr int kStep = kT * kU;
-constexpr int kCap = 512;      // collected entries: two per thread when ranked
+constexpr int kT = kBlock;  // threads of a workgroup
+constexpr int kU = 4;       // 16-byte groups of a step per thread
+constexpr int kCap = 512;   // collected entries
 
 // What a part of a row leaves: M (-inf: no entry), the sums, the entries before
 // the token.
@@ -52,100 +52,77 @@ struct LogprobsArgs {
 
 // ---------------------------------------------------------------- selection ---
 
-// The `keep` largest keys of those offered so far, and some more: keys reach the
-// list when they are at least the bar, which is the keep-th largest key at the
-// time the list was last ranked. Every thread calls every function; what is kept
-// does not depend on the order in which keys arrive.
+// A row's first entries, gathered over segments of it: keys that reach a bar are
+// put into the list as they are met, and the workgroup looks at the list at the
+// end of a segment only, when it is ranked down to its keep largest keys, the last
+// of which is the next segment's bar. What is kept does not depend on the order
+// in which keys arrive.
 struct SelectionLds {
     uint64_t list[kCap];
     uint64_t bar;
-    int counts[3];  // keys offered in a round; rounds take turns
+    int count;  // keys offered, also those that the list had no place for
 };
 
+template <int T>
 struct Selection {
+    static constexpr int kPer = (kCap + T - 1) / T;  // keys that a thread ranks
     SelectionLds& lds;
-    int keep;
-    int n = 0;         // keys in the list, the same in every thread
-    int round = 0;
-    uint64_t bar = 1;  // 0 marks no candidate
+    const int keep;
+    int held = 0;      // keys that earlier segments left in the list, largest first
+    uint64_t bar = 1;  // keys below it are not among the first; 0 marks no key
 
     __device__ Selection(SelectionLds& l, int k) : lds(l), keep(k) {
-        if (threadIdx.x < 3)
-            lds.counts[threadIdx.x] = 0;
-        lds_barrier();
+        if (threadIdx.x == 0)
+            lds.count = 0;
     }
 
-    // f(push) pushes this thread's keys that are at least the bar. Where a round
-    // overflows the list, the keep-th largest key that did fit is a higher bar (the
-    // list holds more than keep keys of this round, and keys are unique): again with that.
-    template <typename F>
-    __device__ void offer(F&& f) {
-        for (;;) {
-            int* count = &lds.counts[round % 3];
-            f([&](uint64_t key) {
-                const int slot = n + atomicAdd(count, 1);
-                if (slot < kCap)
-                    lds.list[slot] = key;
-            });
-            // Of three counters one is written, one may still be read by a thread that
-            // has just passed the barrier before, and one is free.
-            if (threadIdx.x == 0)
-                lds.counts[(round + 1) % 3] = 0;
-            lds_barrier();
-            const int more = *count;
-            ++round;
-            if (n + more <= kCap) {
-                n += more;
-                if (n > 2 * keep + 64)
-                    rank();
-                return;
-            }
-            uint64_t mine[2];
-            int place[2];
-            places(kCap, mine, place);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (place[i] == keep - 1)
-                    lds.bar = mine[i];
-            lds_barrier();
-            bar = lds.bar;
-        }
+    __device__ void put(uint64_t key) {
+        const int slot = atomicAdd(&lds.count, 1);
+        if (slot < kCap)
+            lds.list[slot] = key;
     }
 
-    // The list becomes its keep largest keys, largest first.
-    __device__ void rank() {
-        uint64_t mine[2];
-        int place[2];
-        places(n, mine, place);
+    // After a segment, every thread of the workgroup. False: the list had no place
+    // for some of the segment's keys. The bar is then higher (the keep-th largest key
+    // that did fit: more than keep of them are of this segment, and keys are unique),
+    // and the segment's keys have to be put again.
+    __device__ bool close() {
         lds_barrier();
+        const int n = lds.count;
+        const bool fits = n <= kCap;
+        const int here = fits ? n : kCap;
+        uint64_t mine[kPer];
+        int place[kPer];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (place[i] < keep)
-                lds.list[place[i]] = mine[i];
-        lds_barrier();
-        if (n >= keep) {
-            n = keep;
-            bar = lds.list[keep - 1];
-        }
-    }
-
-    // This thread's keys among the first `held` of the list, and how many of those
-    // are larger (kCap where there is none).
-    __device__ void places(int held, uint64_t (&mine)[2], int (&place)[2]) const {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = static_cast<int>(threadIdx.x) + i * kT;
-            mine[i] = at < held ? lds.list[at] : 0;
+        for (int i = 0; i < kPer; ++i) {
+            const int at = static_cast<int>(threadIdx.x) + i * T;
+            mine[i] = at < here ? lds.list[at] : 0;
             place[i] = kCap;
-            if ((at & ~63) < held) {  // wavefronts without a key have nothing to rank
+            if ((at & ~63) < here) {  // wavefronts without a key have nothing to rank
                 int larger = 0;
 #pragma unroll 8
-                for (int j = 0; j < held; ++j)
+                for (int j = 0; j < here; ++j)
                     larger += lds.list[j] > mine[i];
-                if (at < held)
+                if (at < here)
                     place[i] = larger;
             }
         }
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (fits && place[i] < keep)
+                lds.list[place[i]] = mine[i];
+            if (place[i] == keep - 1)
+                lds.bar = mine[i];
+        }
+        if (fits)
+            held = min(n, keep);
+        if (threadIdx.x == 0)
+            lds.count = held;
+        lds_barrier();
+        if (n >= keep)
+            bar = lds.bar;
+        return fits;
     }
 };
 
@@ -159,50 +136,74 @@ __device__ inline float row_scale(const float* temperature, long row) {
     return temperature_mode(temperature[row], &inv_t) == 1 ? inv_t : __builtin_nanf("");
 }
 
-// (M, S, T) of the same entries against a larger M: T = sum e (x - M).
+// The largest of three; unlike fmaxf it takes no instructions that quiet NaNs (a
+// NaN is lost, or wins: the sums have it).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+template <int W>
+__device__ __forceinline__ float largest(const float (&z)[W]) {
+    if constexpr (W == 8)
+        return max3(max3(z[0], z[1], z[2]), max3(z[3], z[4], z[5]), max3(z[6], z[7], z[7]));
+    else
+        return max3(max3(z[0], z[1], z[2]), z[3], z[3]);
+}
+
+// Sums of e = exp(x - ref) and of e (x - ref) over some entries.
+struct Sums {
+    float ref;
+    double s, t;
+};
+
+// The same against another reference.
 __device__ inline void move_reference(float from, float to, double& s, double& t) {
-    if (from == -__builtin_huge_valf() || from == to)
-        return;  // nothing but entries of -inf so far: the sums are 0 (or NaN)
+    if (from == to || s == 0.0)
+        return;
     const float d = from - to;
     const double f = static_cast<double>(fast_exp2(__builtin_fmaf(d, kLog2e, d * kLog2eLow)));
-    t = f * (t + s * static_cast<double>(d));
+    t = f == 0.0 ? s * f : f * (t + s * static_cast<double>(d));  // d may be -inf; a NaN stays one
     s *= f;
 }
 
-// Joins the threads' parts: in every thread of the first wavefront afterwards.
+// Joins the threads' parts, against the largest entry m: in every thread of the
+// first wavefront afterwards.
+template <int T>
 struct JoinLds {
-    float m[kWaves];
-    int before[kWaves];
-    double s[kWaves], t[kWaves];
+    float m[T / 64];
+    int before[T / 64];
+    double s[T / 64], t[T / 64];
 };
 
-__device__ inline Part join_threads(Part p, JoinLds& lds) {
+template <int T>
+__device__ inline Part join_threads(float m, int before, Sums x, JoinLds<T>& lds) {
     const int wid = threadIdx.x >> 6;
-    float m = wave_max(p.m);
-    move_reference(p.m, m, p.s, p.t);
-    p.s = wave_sum(p.s);
-    p.t = wave_sum(p.t);
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0)
+        lds.m[wid] = m;
+    lds_barrier();
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w)
+        m = fmaxf(m, lds.m[w]);
+    move_reference(x.ref, m, x.s, x.t);
+    x.s = wave_sum(x.s);
+    x.t = wave_sum(x.t);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
-        p.before += __shfl_xor(p.before, off, 64);
+        before += __shfl_xor(before, off, 64);
     if ((threadIdx.x & 63) == 0) {
-        lds.m[wid] = m;
-        lds.before[wid] = p.before;
-        lds.s[wid] = p.s;
-        lds.t[wid] = p.t;
+        lds.before[wid] = before;
+        lds.s[wid] = x.s;
+        lds.t[wid] = x.t;
     }
     lds_barrier();
-    m = lds.m[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w)
-        m = fmaxf(m, lds.m[w]);
     Part out{m, 0, 0.0, 0.0};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        double s = lds.s[w], t = lds.t[w];
-        move_reference(lds.m[w], m, s, t);
-        out.s += s;
-        out.t += t;
+    for (int w = 0; w < T / 64; ++w) {
+        out.s += lds.s[w];
+        out.t += lds.t[w];
         out.before += lds.before[w];
     }
     return out;
@@ -212,6 +213,8 @@ __device__ inline Part join_threads(Part p, JoinLds& lds) {
 __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p, float inv_t, int token,
                                  float z_token, const uint64_t* list, int n) {
     const int tid = threadIdx.x;
+    if (tid >= SPEC_LOGPROBS_MAX_K)
+        return;
     const float inf = __builtin_huge_valf(), nan = __builtin_nanf("");
     const bool empty = p.m == -inf && p.s == 0.0;
     const bool bad = !empty && !(is_finite_f32(p.m) && is_finite_f64(p.s));
@@ -250,150 +253,242 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
     }
 }
 
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kT) void logprobs_kernel(LogprobsArgs a, int splits, int per_split,
-                                                      Part* __restrict__ parts, uint64_t* __restrict__ keys) {
+// Sums over a step are taken against the reference so far as long as their terms
+// stay below this; beyond, the reference becomes the thread's largest entry. A
+// thread without an entry has binary32's lowest value for its reference, whose
+// terms overflow for every entry above it.
+constexpr float kLazy = 256.0f;
+
+template <int DT, int T, int U, bool TOP>
+__global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits, int per_split,
+                                                     Part* __restrict__ parts, uint64_t* __restrict__ keys) {
     using Row = RowGroups<DT>;
     constexpr int W = Row::W;
+    constexpr int kStep = T * U;
     __shared__ SelectionLds select_lds;
-    __shared__ int bars[TOP ? kT + 1 : 1];
-    __shared__ JoinLds join_lds;
+    __shared__ int bars[TOP ? T + 1 : 1];
+    __shared__ JoinLds<T> join_lds;
     const int tid = threadIdx.x;
     const long row = blockIdx.x / static_cast<unsigned>(splits);
     const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(splits));
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
-    const int g0 = min(part * per_split, r.groups);
-    const int g1 = min(g0 + per_split, r.groups);
+    // Steps go over the groups that lie wholly inside the row; what hangs over at its
+    // ends, at most 2 W - 2 entries, are the first part's first threads' own.
+    const int whole = max(r.full1 - r.full0, 0);
+    const int g0 = r.full0 + min(part * per_split, whole);
+    const int g1 = r.full0 + min(part * per_split + per_split, whole);
     const int token = a.token[row];
     const float inv_t = row_scale(a.temperature, row);
-    uint4 next[kU];
+    uint4 next[U];
+    // Groups past the end request the last one, and are put right before they are used
+    // (without a branch: at its end the loads would be waited for).
     auto request = [&](int g) {
-        if (r.full1 > r.full0) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                next[u] = r.request(g + tid + u * kT);
+        for (int u = 0; u < U; ++u)
+            next[u] = r.request_inside(min(g + u * T + tid, g1 - 1));
+    };
+    if (g0 < g1)
+        request(g0);
+    const float inf = __builtin_huge_valf(), nan = __builtin_nanf("");
+    const bool given = token >= 0 && token < a.vocab;
+    const float z_token = given ? r.at_global(token) : nan;  // nothing is larger than or equal to a NaN
+
+    float most = -inf;  // the thread's largest logit
+    Sums sum{kNegMax, 0.0, 0.0};
+    int before = 0;
+    int edge = -1;  // the thread's entry at an end of the row
+    if (part == 0 && tid < a.vocab - whole * W) {
+        edge = tid < (whole ? (W - r.shift) % W : a.vocab) ? tid : tid + whole * W;
+        most = r.at_global(edge);
+        const float x = scale_logit(most, inv_t);
+        if (!(x == -inf))
+            sum = Sums{x, static_cast<double>(fast_exp2(x - x)), 0.0};
+        before = most > z_token || (most == z_token && edge < token);
+    }
+    Selection<T> sel(select_lds, a.keep);
+    float bar_z = kNegMax;  // logits below it are not among the first (-inf never is)
+
+    // Keys of a step's entries that reach the bar.
+    auto collect = [&](const uint4 (&q)[U], const float (&top)[U], int g) {
+        unsigned groups = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            groups |= top[u] >= bar_z ? 1u << u : 0u;
+        while (groups) {
+            const int u = __builtin_ctz(groups);
+            groups &= groups - 1;
+            uint4 x = q[0];
+#pragma unroll
+            for (int i = 1; i < U; ++i) {
+                x.x = u == i ? q[i].x : x.x;
+                x.y = u == i ? q[i].y : x.y;
+                x.z = u == i ? q[i].z : x.z;
+                x.w = u == i ? q[i].w : x.w;
+            }
+            float z[W];
+            Row::unpack(x, z);
+            const int v0 = static_cast<int>(r.element(g + tid + u * T));
+            unsigned hits = 0;
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                hits |= z[e] >= bar_z ? 1u << e : 0u;
+            while (hits) {
+                const int e = __builtin_ctz(hits);
+                hits &= hits - 1;
+                float y = z[0];
+#pragma unroll
+                for (int i = 1; i < W; ++i)
+                    y = e == i ? z[i] : y;
+                const uint64_t key = make_key(y, v0 + e);
+                if (key >= sel.bar)
+                    sel.put(key);
+            }
         }
     };
-    request(g0);
-    const bool given = token >= 0 && token < a.vocab;
-    const float z_token = given ? r.at(token) : 0.0f;
-    // Both zeros are one logit: a token's of +0 is tied by entries of -0.
-    const int token_order = given ? Row::order_of(z_token) - (z_token == 0.0f ? 1 : 0) : 0x7FFFFFFF;
+    auto collect_edge = [&](float z) {
+        if (z >= bar_z && edge >= 0) {
+            const uint64_t key = make_key(z, edge);
+            if (key >= sel.bar)
+                sel.put(key);
+        }
+    };
+    auto settle = [&](uint4 (&q)[U], int g) {
+        if (g + kStep > g1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (g + u * T + tid >= g1)
+                    q[u] = Row::neg_inf();
+        }
+    };
+    auto tops = [&](const uint4 (&q)[U], float (&top)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[W];
+            Row::unpack(q[u], z);
+            top[u] = largest(z);
+        }
+    };
+    // Ends the segment [from, to): its list is ranked, after its keys have been put
+    // again, from memory, as often as the list did not hold them.
+    auto close = [&](int from, int to) {
+        for (;;) {
+            const bool done = sel.close();
+            if (sel.bar > 1)
+                bar_z = key_logit(sel.bar);
+            if (done)
+                return;
+#pragma unroll 1
+            for (int g = from; g < to; g += kStep) {
+                uint4 q[U];
+                float top[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    q[u] = r.request_inside(min(g + u * T + tid, g1 - 1));
+                settle(q, g);
+                tops(q, top);
+                collect(q, top, g);
+            }
+            if (from == g0 && edge >= 0)
+                collect_edge(r.at_global(edge));
+        }
+    };
 
-    const float inf = __builtin_huge_valf();
-    float m = -inf;
-    double s = 0.0, t = 0.0;
-    int before = 0;
-    Selection sel(select_lds, a.keep);
-    // In the order of the logits: below it lie none of the K first entries so far.
-    int bar_o = Row::kOrderNegInf + 1;  // -inf is no candidate
+    int segment = g0, segment_end = g0 + kStep;
 #pragma unroll 1
     for (int g = g0; g < g1; g += kStep) {
-        uint4 q[kU];
+        uint4 q[U];
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
+        for (int u = 0; u < U; ++u)
             q[u] = next[u];
-        r.template settle<kU, kT, false>(g, tid, g1, q);
-        if (g + kStep < g1)
-            request(g + kStep);
+        settle(q, g);
+        request(g + kStep);
 
-        int most[kU];  // the largest of each group, in integer order
-        int best = Row::kOrderNegInf;
+        float top[U];  // the largest of each group
+        float e_sum, t_sum;
+        // exp(x - ref) and its product with x - ref, over the step
+        auto add_up = [&]() {
+            float e[W], t[W];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            most[u] = Row::order_max(q[u]);
-            best = max(best, most[u]);
-        }
-        const float x_best = Row::from_order(best) * inv_t;
-        if (x_best > m) {
-            move_reference(m, x_best, s, t);
-            m = x_best;
-        }
-        const float ref = m == -inf ? 0.0f : m;
+            for (int u = 0; u < U; ++u) {
+                float z[W];
+                Row::unpack(q[u], z);
+                top[u] = largest(z);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            float z[W], e[W], et[W];
-            Row::unpack(q[u], z);
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float d = scale_logit(z[i], inv_t) - ref;
-                e[i] = fast_exp2(d * kLog2e);
-                et[i] = e[i] * fmaxf(d, kNegMax);  // 0 at -inf
+                for (int i = 0; i < W; ++i) {
+                    float d = scale_logit(z[i], inv_t) - sum.ref;
+                    const float x = fast_exp2(d * kLog2e);
+                    d = fmaxf(d, kNegMax);  // 0 times it is 0 at -inf as well
+                    e[i] = u ? e[i] + x : x;
+                    t[i] = u ? __builtin_fmaf(x, d, t[i]) : x * d;
+                }
             }
 #pragma unroll
             for (int n = W / 2; n > 0; n >>= 1)
 #pragma unroll
                 for (int i = 0; i < n; ++i) {
                     e[i] += e[i + n];
-                    et[i] += et[i + n];
+                    t[i] += t[i + n];
                 }
-            s += static_cast<double>(e[0]);
-            t += static_cast<double>(et[0]);
-        }
-        if (best >= token_order) {
+            e_sum = e[0];
+            t_sum = t[0];
+        };
+        add_up();
+        repack(q);
+        float best = top[0];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (most[u] < token_order || g + tid + u * kT >= g1)
+        for (int u = 1; u < U; ++u)
+            best = max3(best, top[u], top[u]);
+        if (!(e_sum <= kLazy)) {
+            const float to = fmaxf(sum.ref, best * inv_t);
+            move_reference(sum.ref, to, sum.s, sum.t);
+            sum.ref = to;
+            add_up();
+            repack(q);
+        }
+        sum.s += static_cast<double>(e_sum);
+        sum.t += static_cast<double>(t_sum);
+
+        if (best >= z_token) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!(top[u] >= z_token) || g + tid + u * T >= g1)
                     continue;
                 float z[W];
                 Row::unpack(q[u], z);
-                const long v0 = r.element(g + tid + u * kT);
+                // ties count at places [0, to) of the group, before the token
+                const long v0 = r.element(g + tid + u * T);
+                const int to = static_cast<int>(v0 + W < token ? W : token - v0);
 #pragma unroll
                 for (int i = 0; i < W; ++i)
-                    before += z[i] > z_token || (z[i] == z_token && v0 + i < token && v0 + i >= 0);
+                    before += z[i] > z_token || (z[i] == z_token && i < to);
             }
         }
         if constexpr (TOP) {
             if (g == g0) {
                 const int held = g1 - g0;
-                bar_o = max(bar_o, bar_of<kT, DT == kBF16 ? 16 : 32>(best, a.keep, held < kT ? held : kT, bars));
+                const int order = bar_of<T, DT == kBF16 ? 16 : 32>(Row::order_of(best), a.keep, held < T ? held : T, bars);
+                bar_z = fmaxf(kNegMax, Row::from_order(order));
+                collect_edge(most);
             }
-            sel.offer([&](auto&& push) {
-                if (sel.bar > 1)
-                    bar_o = max(bar_o, Row::order_of(key_logit(sel.bar)));
-                const int from = bar_o == 0 ? -1 : bar_o;  // a bar at +0 lets -0 through
-                const float from_z = Row::from_order(from);
-                unsigned groups = 0;
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    groups |= most[u] >= from ? 1u << u : 0u;
-                while (groups) {
-                    const int u = __builtin_ctz(groups);
-                    groups &= groups - 1;
-                    uint4 x = q[0];
-#pragma unroll
-                    for (int i = 1; i < kU; ++i) {
-                        x.x = u == i ? q[i].x : x.x;
-                        x.y = u == i ? q[i].y : x.y;
-                        x.z = u == i ? q[i].z : x.z;
-                        x.w = u == i ? q[i].w : x.w;
-                    }
-                    float z[W];
-                    Row::unpack(x, z);
-                    const int v0 = static_cast<int>(r.element(g + tid + u * kT));
-                    unsigned hits = 0;
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        hits |= z[e] >= from_z ? 1u << e : 0u;
-                    while (hits) {
-                        const int e = __builtin_ctz(hits);
-                        hits &= hits - 1;
-                        float y = z[0];
-#pragma unroll
-                        for (int i = 1; i < W; ++i)
-                            y = e == i ? z[i] : y;
-                        const uint64_t key = make_key(y, v0 + e);
-                        if (key >= sel.bar)
-                            push(key);
-                    }
-                }
-            });
+            if (best >= bar_z)
+                collect(q, top, g);
+            // Segments of 1, 1, 2, 4, .. steps: each doubles what has been seen, and lets
+            // about keep new keys through.
+            if (g + kStep >= segment_end || g + kStep >= g1) {
+                close(segment, min(segment_end, g1));
+                segment_end += segment_end - g0;
+                segment = g + kStep;
+            }
         }
+        most = max3(most, best, best);
     }
-    if (TOP)
-        sel.rank();
-    const Part p = join_threads(Part{m, before, s, t}, join_lds);
-    const int n = min(sel.n, a.keep);
+    if (TOP && g0 == g1) {  // a row of no whole group, or a part behind the row's end
+        __syncthreads();
+        collect_edge(most);
+        sel.close();
+    }
+    const Part p = join_threads<T>(most * inv_t, before, sum, join_lds);
+    const int n = sel.held;
     if (splits == 1) {
         write_row(a, row, p, inv_t, token, z_token, select_lds.list, n);
         return;
@@ -411,34 +506,56 @@ __global__ __launch_bounds__(kT) void logprobs_merge_kernel(LogprobsArgs a, int 
                                                             const Part* __restrict__ parts,
                                                             const uint64_t* __restrict__ keys) {
     __shared__ SelectionLds select_lds;
-    __shared__ JoinLds join_lds;
+    __shared__ int bars[kT + 1];
+    __shared__ JoinLds<kT> join_lds;
     const int tid = threadIdx.x;
     const long row = blockIdx.x;
+    const int total = splits * a.keep;
+    const uint64_t* row_keys = keys + row * total;
+    constexpr int kHeld = 4;  // keys of a thread in registers
+    uint64_t own[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        own[i] = tid + i * kT < total ? row_keys[tid + i * kT] : 0;
     const int token = a.token[row];
     const float inv_t = row_scale(a.temperature, row);
     const RowGroups<DT> r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
-    const float z_token = token >= 0 && token < a.vocab ? r.at(token) : 0.0f;
-    Part p{-__builtin_huge_valf(), 0, 0.0, 0.0};
+    const float z_token = token >= 0 && token < a.vocab ? r.at_global(token) : 0.0f;
+    float m = -__builtin_huge_valf();
+    Sums sum{m, 0.0, 0.0};
+    int before = 0;
     for (int i = tid; i < splits; i += kT) {
         Part x = parts[row * splits + i];
-        const float m = fmaxf(p.m, x.m);
-        move_reference(p.m, m, p.s, p.t);
+        m = fmaxf(sum.ref, x.m);
+        move_reference(sum.ref, m, sum.s, sum.t);
         move_reference(x.m, m, x.s, x.t);
-        p = Part{m, p.before + x.before, p.s + x.s, p.t + x.t};
+        sum = Sums{m, sum.s + x.s, sum.t + x.t};
+        before += x.before;
     }
-    Selection sel(select_lds, a.keep);
-    const int total = splits * a.keep;
-    for (int i0 = 0; i0 < total; i0 += kT) {
-        const uint64_t key = i0 + tid < total ? keys[row * total + i0 + tid] : 0;
-        sel.offer([&](auto&& push) {
-            if (key >= sel.bar)
-                push(key);
-        });
+    Selection<kT> sel(select_lds, a.keep);
+    if (a.keep) {
+        uint64_t best = own[0];
+#pragma unroll
+        for (int i = 1; i < kHeld; ++i)
+            best = own[i] > best ? own[i] : best;
+        // the upper half of a key rises with the logit; 0, no key, is the lowest
+        const int bar = bar_of<kT, 32>(static_cast<int>(static_cast<uint32_t>(best >> 32) ^ 0x80000000u), a.keep,
+                                       total < kT ? total : kT, bars);
+        const uint64_t least = static_cast<uint64_t>(static_cast<uint32_t>(bar) ^ 0x80000000u) << 32;
+        do {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                if (own[i] >= sel.bar && own[i] >= least)
+                    sel.put(own[i]);
+            for (int i = tid + kHeld * kT; i < total; i += kT) {
+                const uint64_t key = row_keys[i];
+                if (key >= sel.bar && key >= least)
+                    sel.put(key);
+            }
+        } while (!sel.close());
     }
-    if (a.keep)
-        sel.rank();
-    p = join_threads(p, join_lds);
-    write_row(a, row, p, inv_t, token, z_token, select_lds.list, min(sel.n, a.keep));
+    const Part p = join_threads<kT>(m, before, sum, join_lds);
+    write_row(a, row, p, inv_t, token, z_token, select_lds.list, sel.held);
 }
 
 // ---------------------------------------------------------------- backward ---
@@ -538,6 +655,7 @@ struct Split {
 
 Split split_of(int rows, int vocab, int dtype) {
     const long groups = static_cast<long>(vocab) / (dtype == SPEC_BF16 ? 8 : 4) + 2;  // at any alignment
+    constexpr long kStep = kT * kU;
     const long steps = (groups + kStep - 1) / kStep;
     const long want = (1024 + rows - 1) / rows;
     const long per = (steps + want - 1) / want;
@@ -627,7 +745,7 @@ int spec_token_logprobs(spec_logprobs_ctx* ctx, int rows, const void* logits, co
     const dim3 grid(static_cast<unsigned>(static_cast<long>(rows) * p.splits)), block(kT);
     hipStream_t s = ctx->stream;
 #define SPEC_LOGPROBS(DT, TOP) \
-    logprobs_kernel<DT, TOP><<<grid, block, 0, s>>>(a, p.splits, p.per_split, ctx->parts, ctx->keys)
+    logprobs_kernel<DT, kT, kU, TOP><<<grid, block, 0, s>>>(a, p.splits, p.per_split, ctx->parts, ctx->keys)
     const bool bf16 = ctx->dtype == SPEC_BF16;
     if (ctx->K)
         bf16 ? SPEC_LOGPROBS(kBF16, true) : SPEC_LOGPROBS(kF32, true);

@@ -100,6 +100,20 @@ struct RowGroups {
         return make_uint4(v.x, v.y, v.z, v.w);
     }
 
+    // Group g, which lies wholly inside the row; its address space is named, for where
+    // the compiler does not find it out.
+    __device__ __forceinline__ uint4 request_inside(int g) const {
+        typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+        typedef const __attribute__((address_space(1))) u32x4* global_t;
+        const u32x4 v = __builtin_nontemporal_load((global_t)(reinterpret_cast<const u32x4*>(base) + g));
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
+    __device__ __forceinline__ float at_global(long v) const {
+        typedef const __attribute__((address_space(1))) elem_t* global_t;
+        const uint32_t b = *(global_t)(reinterpret_cast<const elem_t*>(start) + v);
+        return __uint_as_float(DT == kBF16 ? b << 16 : b);
+    }
+
     __device__ uint4 load_any(int g, int end) const {
         if (g >= end)
             return neg_inf();
