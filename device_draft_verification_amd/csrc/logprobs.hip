@@ -27,10 +27,9 @@ namespace {
 
 constexpr int kT = kBlock;  // threads of a workgroup
 constexpr int kU = 4;       // 16-byte groups of a step per thread
-constexpr int kCap = 512;   // collected entries
 
-// What a part of a row leaves: M (-inf: no entry), the sums, the entries before
-// the token.
+// What a part of a row leaves: M (-inf: no entry), S and T = sum e (x - M) log2e, the
+// entries before the token.
 struct Part {
     float m;
     int before;
@@ -52,77 +51,199 @@ struct LogprobsArgs {
 
 // ---------------------------------------------------------------- selection ---
 
-// A row's first entries, gathered over segments of it: keys that reach a bar are
-// put into the list as they are met, and the workgroup looks at the list at the
-// end of a segment only, when it is ranked down to its keep largest keys, the last
-// of which is the next segment's bar. What is kept does not depend on the order
-// in which keys arrive.
-struct SelectionLds {
-    uint64_t list[kCap];
-    uint64_t bar;
-    int count;  // keys offered, also those that the list had no place for
-};
+// The wavefront's lanes below this one that are in the mask.
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+    return static_cast<int>(__builtin_amdgcn_mbcnt_hi(
+        static_cast<uint32_t>(mask >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0)));
+}
+
+// The upper half of a key, which rises with the logit, as the logit; its last bits
+// may be missing (the result is then lower, or the lowest number).
+__device__ inline float logit_at_least(uint32_t upper) {
+    return upper < ordered32(kNegMax) ? kNegMax : unordered32(upper);
+}
+
+// The k-th largest of 64 N numbers, N in each lane (of the first n chunks), the same
+// in every lane, with the bits below LOW zero: its bits from the top, each by as many
+// ballots as there are chunks.
+template <int N, int LOW>
+__device__ inline uint32_t kth_largest(const uint32_t (&v)[N], int n, int k) {
+    uint32_t t = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= LOW; --bit) {
+        const uint32_t up = t | 1u << bit;
+        int reach = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n)
+                reach += __popcll(__ballot(v[i] >= up));
+        t = reach >= k ? up : t;
+    }
+    return t;
+}
+
+// A row's first entries, gathered over segments of it. While a segment goes by,
+// each wavefront puts the 16-byte groups aside whose largest entry reaches a bar (few
+// do, and single entries would cost all lanes the way through them); at its end
+// their entries that reach the bar become keys in a list of the workgroup's, and the
+// list's keep-th largest is the next segment's bar. What is kept does not depend on
+// the order in which keys arrive.
+constexpr int kCap = 512;  // keys
 
 template <int T>
+struct SelectionLds {
+    alignas(16) uint64_t lists[2][kCap];
+    uint64_t bar;
+    int counts[2];     // keys put into the lists, also those that one had no place for
+    int lost;          // groups that a wavefront had no place for
+    uint32_t most[T];  // the threads' largest entries
+};
+
+template <int T, int G>
+struct GroupLds {
+    uint4 data[T / 64][G];
+    int at[T / 64][G];
+};
+
+// LOW: bits of a key's upper half that need not be looked at.
+template <int T, int LOW>
 struct Selection {
-    static constexpr int kPer = (kCap + T - 1) / T;  // keys that a thread ranks
-    SelectionLds& lds;
+    SelectionLds<T>& lds;
     const int keep;
-    int held = 0;      // keys that earlier segments left in the list, largest first
+    int cur = 0;       // the list in use
+    int held = 0;      // keys that earlier segments left in it
     uint64_t bar = 1;  // keys below it are not among the first; 0 marks no key
 
-    __device__ Selection(SelectionLds& l, int k) : lds(l), keep(k) {
+    __device__ Selection(SelectionLds<T>& l, int k) : lds(l), keep(k) {
         if (threadIdx.x == 0)
-            lds.count = 0;
-    }
-
-    __device__ void put(uint64_t key) {
-        const int slot = atomicAdd(&lds.count, 1);
-        if (slot < kCap)
-            lds.list[slot] = key;
-    }
-
-    // After a segment, every thread of the workgroup. False: the list had no place
-    // for some of the segment's keys. The bar is then higher (the keep-th largest key
-    // that did fit: more than keep of them are of this segment, and keys are unique),
-    // and the segment's keys have to be put again.
-    __device__ bool close() {
+            lds.counts[0] = lds.counts[1] = lds.lost = 0;
         lds_barrier();
-        const int n = lds.count;
-        const bool fits = n <= kCap;
-        const int here = fits ? n : kCap;
-        uint64_t mine[kPer];
-        int place[kPer];
+    }
+
+    // Each lane's key, where it has one, into list `to`; the whole wavefront calls it.
+    __device__ void put(bool has, uint64_t key, int to) {
+        const uint64_t mask = __ballot(has);
+        if (mask == 0)
+            return;
+        int base = 0;
+        if ((threadIdx.x & 63) == 0)
+            base = atomicAdd(&lds.counts[to], __popcll(mask));
+        const int slot = __builtin_amdgcn_readfirstlane(base) + lanes_below(mask);
+        if (has && slot < kCap)
+            lds.lists[to][slot] = key;
+    }
+
+    // A first bar: that of the threads' largest entries.
+    __device__ void begin(float most) {
+        lds.most[threadIdx.x] = ordered32(most + 0.0f);
+        lds_barrier();
+        uint32_t v[T / 64];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < T / 64; ++i)
+            v[i] = lds.most[threadIdx.x % 64 + 64 * i];
+        raise(static_cast<uint64_t>(kth_largest<T / 64, LOW>(v, T / 64, keep)) << 32);
+    }
+
+    __device__ void raise(uint64_t to) { bar = to > bar ? to : bar; }
+
+    // After a segment, every thread of the workgroup: f() puts the wavefront's keys
+    // that are at least the bar into list `cur`. False: groups were lost, and nothing
+    // has changed.
+    template <typename F>
+    __device__ bool close(F&& f) {
+        int n;
+        for (;;) {
+            f();
+            lds_barrier();
+            n = lds.counts[cur];
+            const bool lost = lds.lost != 0;
+            if (n <= kCap && !lost)
+                break;
+            // Of the keys that did fit, more than keep are the segment's, and keys are
+            // unique: the keep-th largest is a higher bar.
+            if (!lost)
+                rank(kCap);
+            lds_barrier();
+            if (!lost)
+                bar = lds.bar;
+            if (threadIdx.x == 0) {
+                lds.counts[cur] = held;
+                lds.lost = 0;
+            }
+            lds_barrier();
+            if (lost)
+                return false;
+        }
+        held = n;
+        if (n > keep + 16)
+            narrow();
+        if (held > keep + 64)  // that many are equal
+            sort();
+        return true;
+    }
+
+    // The list's keys that are at least its keep-th largest, into the other list.
+    __device__ void narrow() {
+        constexpr int N = kCap / 64;
+        const int lane = threadIdx.x & 63, chunks = (held + 63) / 64;
+        uint64_t key[N];
+        uint32_t v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            key[i] = i < chunks && 64 * i + lane < held ? lds.lists[cur][64 * i + lane] : 0;
+            v[i] = static_cast<uint32_t>(key[i] >> 32);
+        }
+        raise(static_cast<uint64_t>(kth_largest<N, LOW>(v, chunks, keep)) << 32);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < chunks && i % (T / 64) == static_cast<int>(threadIdx.x >> 6))
+                put(key[i] >= bar, key[i], cur ^ 1);
+        swap();
+    }
+
+    // The list becomes its keep largest keys, largest first.
+    __device__ void sort() {
+        rank(held);
+        if (threadIdx.x == 0)
+            lds.counts[cur ^ 1] = min(held, keep);
+        swap();
+        if (held >= keep)
+            bar = lds.lists[cur][keep - 1];
+    }
+
+    __device__ void swap() {
+        lds_barrier();
+        cur ^= 1;
+        held = lds.counts[cur];
+        if (threadIdx.x == 0)
+            lds.counts[cur ^ 1] = 0;  // seen by all behind the next barrier, before its next use
+    }
+
+    // The keep largest of the list's first n keys, largest first, into the other list.
+    __device__ void rank(int n) const {
+        const uint64_t* list = lds.lists[cur];
+#pragma unroll
+        for (int i = 0; i < (kCap + T - 1) / T; ++i) {
             const int at = static_cast<int>(threadIdx.x) + i * T;
-            mine[i] = at < here ? lds.list[at] : 0;
-            place[i] = kCap;
-            if ((at & ~63) < here) {  // wavefronts without a key have nothing to rank
-                int larger = 0;
-#pragma unroll 8
-                for (int j = 0; j < here; ++j)
-                    larger += lds.list[j] > mine[i];
-                if (at < here)
-                    place[i] = larger;
+            if ((at & ~63) >= n)
+                continue;  // wavefronts without a key have nothing to rank
+            const uint64_t mine = at < n ? list[at] : ~0ull;
+            int larger = 0, j = 0;
+            for (; j + 16 <= n; j += 16)
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + j + k);
+                    larger += two.x > mine;
+                    larger += two.y > mine;
+                }
+            for (; j < n; ++j)
+                larger += list[j] > mine;
+            if (at < n && larger < keep) {
+                lds.lists[cur ^ 1][larger] = mine;
+                if (larger == keep - 1)
+                    lds.bar = mine;
             }
         }
-        lds_barrier();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (fits && place[i] < keep)
-                lds.list[place[i]] = mine[i];
-            if (place[i] == keep - 1)
-                lds.bar = mine[i];
-        }
-        if (fits)
-            held = min(n, keep);
-        if (threadIdx.x == 0)
-            lds.count = held;
-        lds_barrier();
-        if (n >= keep)
-            bar = lds.bar;
-        return fits;
     }
 };
 
@@ -144,6 +265,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// The larger of two, a NaN if either is.
+__device__ __forceinline__ float maximum(float a, float b) {
+    float r;
+    asm("v_maximum3_f32 %0, %1, %2, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+// A value that is the same in the whole wavefront, known to be so.
+__device__ __forceinline__ float uniform(float v) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
 template <int W>
 __device__ __forceinline__ float largest(const float (&z)[W]) {
     if constexpr (W == 8)
@@ -152,24 +285,44 @@ __device__ __forceinline__ float largest(const float (&z)[W]) {
         return max3(max3(z[0], z[1], z[2]), z[3], z[3]);
 }
 
-// Sums of e = exp(x - ref) and of e (x - ref) over some entries.
+// Sums of e = 2^y and of e y over some entries, y their distance from a reference in
+// units of ln 2. Near the origin (see kReach) the reference is a value of x log2e,
+// rounded to binary32, and y one multiply-add; a far one is a value of x itself,
+// since beside it x log2e has no digits left for the distances.
 struct Sums {
     float ref;
+    bool far;
     double s, t;
 };
 
-// The same against another reference.
-__device__ inline void move_reference(float from, float to, double& s, double& t) {
-    if (from == to || s == 0.0)
-        return;
-    const float d = from - to;
-    const double f = static_cast<double>(fast_exp2(__builtin_fmaf(d, kLog2e, d * kLog2eLow)));
-    t = f == 0.0 ? s * f : f * (t + s * static_cast<double>(d));  // d may be -inf; a NaN stays one
-    s *= f;
+// How far reference `from` lies above `to`, in the same units.
+__device__ inline double reference_step(float from, bool from_far, float to, bool to_far) {
+    const double a = static_cast<double>(from), b = static_cast<double>(to), c = static_cast<double>(kLog2e);
+    if (from_far && to_far)
+        return (a - b) * c;
+    return (from_far ? a * c : a) - (to_far ? b * c : b);
 }
 
-// Joins the threads' parts, against the largest entry m: in every thread of the
-// first wavefront afterwards.
+__device__ inline void move_reference(Sums& x, float to, bool to_far) {
+    const double d = reference_step(x.ref, x.far, to, to_far);
+    x.ref = to;
+    x.far = to_far;
+    if (d == 0.0 || x.s == 0.0)
+        return;
+    const double f = static_cast<double>(fast_exp2(static_cast<float>(d)));
+    x.t = f == 0.0 ? x.s * f : f * (x.t + x.s * d);  // a NaN stays one
+    x.s *= f;
+}
+
+// Beyond it binary32 rounds x log2e by more than 2^-3.
+constexpr float kReach = 1048576.0f;
+
+// A group's sums are taken against the wavefront's reference so far as long as they
+// stay below this; beyond, the reference becomes its largest entry so far.
+constexpr float kLazy = 256.0f;
+
+// Joins the threads' parts and single entries edge_x (-inf: none), against the
+// largest entry m: in every thread afterwards.
 template <int T>
 struct JoinLds {
     float m[T / 64];
@@ -178,7 +331,7 @@ struct JoinLds {
 };
 
 template <int T>
-__device__ inline Part join_threads(float m, int before, Sums x, JoinLds<T>& lds) {
+__device__ inline Part join_threads(float m, int before, Sums x, float edge_x, JoinLds<T>& lds) {
     const int wid = threadIdx.x >> 6;
     m = wave_max(m);
     if ((threadIdx.x & 63) == 0)
@@ -187,7 +340,12 @@ __device__ inline Part join_threads(float m, int before, Sums x, JoinLds<T>& lds
 #pragma unroll
     for (int w = 0; w < T / 64; ++w)
         m = fmaxf(m, lds.m[w]);
-    move_reference(x.ref, m, x.s, x.t);
+    move_reference(x, m, true);
+    if (!(edge_x == -__builtin_huge_valf())) {
+        const float d = (edge_x - m) * kLog2e, e = fast_exp2(d);
+        x.s += static_cast<double>(e);
+        x.t += static_cast<double>(e * fmaxf(d, kNegMax));
+    }
     x.s = wave_sum(x.s);
     x.t = wave_sum(x.t);
 #pragma unroll
@@ -233,7 +391,7 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
         }
         a.out_logprob[row] = bad ? nan : lp;
         a.out_rank[row] = bad ? -1 : rank;
-        a.out_entropy[row] = bad ? nan : empty ? 0.0f : fmaxf(static_cast<float>(log_s - p.t / p.s), 0.0f);
+        a.out_entropy[row] = bad ? nan : empty ? 0.0f : fmaxf(static_cast<float>(log_s - p.t / p.s / static_cast<double>(kLog2e)), 0.0f);
         a.out_norm[2 * row] = bad ? nan : p.m;
         a.out_norm[2 * row + 1] = bad ? nan : static_cast<float>(log_s);
     }
@@ -253,22 +411,19 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
     }
 }
 
-// Sums over a step are taken against the reference so far as long as their terms
-// stay below this; beyond, the reference becomes the thread's largest entry. A
-// thread without an entry has binary32's lowest value for its reference, whose
-// terms overflow for every entry above it.
-constexpr float kLazy = 256.0f;
-
 template <int DT, int T, int U, bool TOP>
 __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits, int per_split,
                                                      Part* __restrict__ parts, uint64_t* __restrict__ keys) {
     using Row = RowGroups<DT>;
     constexpr int W = Row::W;
     constexpr int kStep = T * U;
-    __shared__ SelectionLds select_lds;
-    __shared__ int bars[TOP ? T + 1 : 1];
+    constexpr int kAside = 64 * U;  // a wavefront's groups of a step
+    using Select = Selection<T, DT == kBF16 ? 16 : 12>;
+    __shared__ typename std::conditional<TOP, SelectionLds<T>, int>::type select_lds;
+    __shared__ typename std::conditional<TOP, GroupLds<T, kAside>, int>::type aside;
     __shared__ JoinLds<T> join_lds;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const long row = blockIdx.x / static_cast<unsigned>(splits);
     const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(splits));
     const Row r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
@@ -279,225 +434,235 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits,
     const int g1 = r.full0 + min(part * per_split + per_split, whole);
     const int token = a.token[row];
     const float inv_t = row_scale(a.temperature, row);
-    uint4 next[U];
-    // Groups past the end request the last one, and are put right before they are used
+    const bool unit = inv_t == 1.0f;
+    uint4 q[U];
+    // Groups past the end request the last one, and are put right when they are used
     // (without a branch: at its end the loads would be waited for).
-    auto request = [&](int g) {
+    auto request = [&](int g) { return r.request_inside(min(g + tid, g1 - 1)); };
+    if (g0 < g1) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            next[u] = r.request_inside(min(g + u * T + tid, g1 - 1));
-    };
-    if (g0 < g1)
-        request(g0);
+            q[u] = request(g0 + u * T);
+    }
     const float inf = __builtin_huge_valf(), nan = __builtin_nanf("");
     const bool given = token >= 0 && token < a.vocab;
     const float z_token = given ? r.at_global(token) : nan;  // nothing is larger than or equal to a NaN
+    // Entries before the token in the order are those above z_token, and in front of it
+    // those above the next number below: not (z <= NaN) is true of -inf as well.
+    const float z_front = z_token == -inf ? nan : from_order32(z_token == 0.0f ? -2 : order32(z_token) - 1);
+    const int token_group = given ? static_cast<int>(r.group_of(token)) : 0;
 
-    float most = -inf;  // the thread's largest logit
-    Sums sum{kNegMax, 0.0, 0.0};
-    int before = 0;
-    int edge = -1;  // the thread's entry at an end of the row
-    if (part == 0 && tid < a.vocab - whole * W) {
+    float most = -inf;         // the thread's largest logit
+    int before = 0, ties = 0;  // the wavefront's entries before the token, the thread's others
+    int edge = 0;
+    if (part == 0 && tid < a.vocab - whole * W) {  // an entry at an end of the row
         edge = tid < (whole ? (W - r.shift) % W : a.vocab) ? tid : tid + whole * W;
         most = r.at_global(edge);
-        const float x = scale_logit(most, inv_t);
-        if (!(x == -inf))
-            sum = Sums{x, static_cast<double>(fast_exp2(x - x)), 0.0};
-        before = most > z_token || (most == z_token && edge < token);
+        ties = most > z_token || (most == z_token && edge < token);
     }
-    Selection<T> sel(select_lds, a.keep);
-    float bar_z = kNegMax;  // logits below it are not among the first (-inf never is)
+    const float edge_z = most, edge_x = most * inv_t;
 
-    // Keys of a step's entries that reach the bar.
-    auto collect = [&](const uint4 (&q)[U], const float (&top)[U], int g) {
-        unsigned groups = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            groups |= top[u] >= bar_z ? 1u << u : 0u;
-        while (groups) {
-            const int u = __builtin_ctz(groups);
-            groups &= groups - 1;
-            uint4 x = q[0];
-#pragma unroll
-            for (int i = 1; i < U; ++i) {
-                x.x = u == i ? q[i].x : x.x;
-                x.y = u == i ? q[i].y : x.y;
-                x.z = u == i ? q[i].z : x.z;
-                x.w = u == i ? q[i].w : x.w;
-            }
-            float z[W];
-            Row::unpack(x, z);
-            const int v0 = static_cast<int>(r.element(g + tid + u * T));
-            unsigned hits = 0;
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                hits |= z[e] >= bar_z ? 1u << e : 0u;
-            while (hits) {
-                const int e = __builtin_ctz(hits);
-                hits &= hits - 1;
-                float y = z[0];
-#pragma unroll
-                for (int i = 1; i < W; ++i)
-                    y = e == i ? z[i] : y;
-                const uint64_t key = make_key(y, v0 + e);
-                if (key >= sel.bar)
-                    sel.put(key);
-            }
-        }
-    };
-    auto collect_edge = [&](float z) {
-        if (z >= bar_z && edge >= 0) {
-            const uint64_t key = make_key(z, edge);
-            if (key >= sel.bar)
-                sel.put(key);
-        }
-    };
-    auto settle = [&](uint4 (&q)[U], int g) {
-        if (g + kStep > g1) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (g + u * T + tid >= g1)
-                    q[u] = Row::neg_inf();
-        }
-    };
-    auto tops = [&](const uint4 (&q)[U], float (&top)[U]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float z[W];
-            Row::unpack(q[u], z);
-            top[u] = largest(z);
-        }
-    };
-    // Ends the segment [from, to): its list is ranked, after its keys have been put
-    // again, from memory, as often as the list did not hold them.
-    auto close = [&](int from, int to) {
+    // The wavefront's reference in units of x (-inf: none yet, which is the far one of
+    // binary32's lowest value), and whether it has met entries of -inf.
+    float ref_x = -inf;
+    bool holes = false;
+    Sums sum{kNegMax, true, 0.0, 0.0};
+    float s_group = 0.0f, t_group = 0.0f;  // of a step, added to sum at its end
+    float bar_z = kNegMax;                 // logits below it are not among the first (-inf never is)
+    int put_aside = 0;                     // groups, by this wavefront
+
+    // A group's sums, of scaled logits x.
+    auto add_up = [&](const float (&x)[W], float top) {
         for (;;) {
-            const bool done = sel.close();
-            if (sel.bar > 1)
-                bar_z = key_logit(sel.bar);
-            if (done)
-                return;
-#pragma unroll 1
-            for (int g = from; g < to; g += kStep) {
-                uint4 q[U];
-                float top[U];
+            float d[W], e[W];
+            if (sum.far) {
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    q[u] = r.request_inside(min(g + u * T + tid, g1 - 1));
-                settle(q, g);
-                tops(q, top);
-                collect(q, top, g);
+                for (int i = 0; i < W; ++i)
+                    d[i] = (x[i] - sum.ref) * kLog2e;
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    d[i] = __builtin_fmaf(x[i], kLog2e, -sum.ref);
             }
-            if (from == g0 && edge >= 0)
-                collect_edge(r.at_global(edge));
-        }
-    };
-
-    int segment = g0, segment_end = g0 + kStep;
-#pragma unroll 1
-    for (int g = g0; g < g1; g += kStep) {
-        uint4 q[U];
+            if (holes) {  // 0 times the lowest value is 0; a NaN stays one
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            q[u] = next[u];
-        settle(q, g);
-        request(g + kStep);
-
-        float top[U];  // the largest of each group
-        float e_sum, t_sum;
-        // exp(x - ref) and its product with x - ref, over the step
-        auto add_up = [&]() {
-            float e[W], t[W];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float z[W];
-                Row::unpack(q[u], z);
-                top[u] = largest(z);
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    float d = scale_logit(z[i], inv_t) - sum.ref;
-                    const float x = fast_exp2(d * kLog2e);
-                    d = fmaxf(d, kNegMax);  // 0 times it is 0 at -inf as well
-                    e[i] = u ? e[i] + x : x;
-                    t[i] = u ? __builtin_fmaf(x, d, t[i]) : x * d;
-                }
+                for (int i = 0; i < W; ++i)
+                    d[i] = maximum(d[i], kNegMax);
             }
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                e[i] = fast_exp2(d[i]);
+            float t = e[0] * d[0], t2 = e[1] * d[1];
+#pragma unroll
+            for (int i = 2; i < W; i += 2) {
+                t = __builtin_fmaf(e[i], d[i], t);
+                t2 = __builtin_fmaf(e[i + 1], d[i + 1], t2);
+            }
+            t += t2;
 #pragma unroll
             for (int n = W / 2; n > 0; n >>= 1)
 #pragma unroll
-                for (int i = 0; i < n; ++i) {
+                for (int i = 0; i < n; ++i)
                     e[i] += e[i + n];
-                    t[i] += t[i + n];
+            const float s = e[0];
+            // the same in the whole wavefront, and no more often than there are causes
+            if (__ballot(!(s <= kLazy) || !(t == t))) {
+                if (!holes && __ballot(!(t == t))) {  // an entry of -inf; more are likely
+                    holes = true;
+                    continue;
                 }
-            e_sum = e[0];
-            t_sum = t[0];
-        };
-        add_up();
-        repack(q);
-        float best = top[0];
-#pragma unroll
-        for (int u = 1; u < U; ++u)
-            best = max3(best, top[u], top[u]);
-        if (!(e_sum <= kLazy)) {
-            const float to = fmaxf(sum.ref, best * inv_t);
-            move_reference(sum.ref, to, sum.s, sum.t);
-            sum.ref = to;
-            add_up();
-            repack(q);
+                const float best = uniform(wave_max(max3(most, top, top)) * inv_t);
+                if (best > ref_x) {
+                    ref_x = best;
+                    sum.s += static_cast<double>(s_group);
+                    sum.t += static_cast<double>(t_group);
+                    s_group = t_group = 0.0f;
+                    const bool far = !(fabsf(best) < kReach);
+                    move_reference(sum, far ? best : best * kLog2e, far);
+                    continue;
+                }
+            }
+            s_group += s;
+            t_group += t;
+            return;
         }
-        sum.s += static_cast<double>(e_sum);
-        sum.t += static_cast<double>(t_sum);
+    };
+    // The wavefront's groups that reach the bar are put aside.
+    auto collect = [&](const uint4& x, float top, int at) {
+        if constexpr (TOP) {
+            const uint64_t mask = __ballot(top >= bar_z);
+            if (mask) {
+                const int slot = put_aside + lanes_below(mask);
+                if (top >= bar_z && slot < kAside) {
+                    aside.data[wid][slot] = x;
+                    aside.at[wid][slot] = at;
+                }
+                put_aside += __popcll(mask);
+            }
+        }
+    };
 
-        if (best >= z_token) {
+    auto body = [&](auto& sel) {
+        // Ends the segment [from, to). If it had more groups than there is place for, its
+        // steps are gone through again, from memory, each as a segment.
+        auto close = [&](int from, int to) {
+            if constexpr (TOP) {
+                auto end = [&](bool first) {
+                    if (put_aside > kAside)
+                        select_lds.lost = 1;
+                    if (first)
+                        sel.begin(most);
+                    const bool done = sel.close([&]() {
+#pragma unroll 1
+                        for (int i0 = 0; i0 < min(put_aside, kAside); i0 += 64) {
+                            const int i = i0 + lane;
+                            const bool mine = i < min(put_aside, kAside);
+                            float z[W];
+                            Row::unpack(mine ? aside.data[wid][i] : Row::neg_inf(), z);
+                            const int v0 = mine ? static_cast<int>(r.element(aside.at[wid][i])) : 0;
+#pragma unroll
+                            for (int e = 0; e < W; ++e) {
+                                const uint64_t key = make_key(z[e], v0 + e);
+                                sel.put(z[e] >= kNegMax && key >= sel.bar, key, sel.cur);
+                            }
+                        }
+                        if (first) {
+                            const uint64_t key = make_key(edge_z, edge);
+                            sel.put(edge_z >= kNegMax && key >= sel.bar, key, sel.cur);
+                        }
+                    });
+                    put_aside = 0;
+                    bar_z = logit_at_least(static_cast<uint32_t>(sel.bar >> 32));
+                    return done;
+                };
+                if (end(from == g0))
+                    return;
+#pragma unroll 1
+                for (int g = from; g < to; g += kStep) {
+#pragma unroll 1
+                    for (int u = 0; u < U; ++u) {
+                        const int at = g + u * T + tid;
+                        const uint4 x = at < g1 ? r.request_inside(at) : Row::neg_inf();
+                        float z[W];
+                        Row::unpack(x, z);
+                        collect(x, largest(z), at);
+                    }
+                    end(g == g0);
+                }
+            }
+        };
+
+        int segment = g0, segment_end = g0 + kStep;
+#pragma unroll 1
+        for (int g = g0; g < g1; g += kStep) {
+            const bool last = g + kStep > g1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!(top[u] >= z_token) || g + tid + u * T >= g1)
-                    continue;
+                const int at = g + u * T + tid;
+                uint4 x = q[u];
+                if (last && at >= g1)
+                    x = Row::neg_inf();
                 float z[W];
-                Row::unpack(q[u], z);
-                // ties count at places [0, to) of the group, before the token
-                const long v0 = r.element(g + tid + u * T);
-                const int to = static_cast<int>(v0 + W < token ? W : token - v0);
+                Row::unpack(x, z);
+                const float top = largest(z);
+                collect(x, top, at);
+                q[u] = request(g + kStep + u * T);
+                if (__ballot(top >= z_token)) {
+                    const float above = at >= g1 ? inf : at < token_group ? z_front : z_token;
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    before += z[i] > z_token || (z[i] == z_token && i < to);
+                    for (int i = 0; i < W; ++i)
+                        before += static_cast<int>(__popcll(__ballot(!(z[i] <= above))));
+                    if (at == token_group) {  // ties in front of the token in its own group
+                        const int to = static_cast<int>(token - r.element(at));
+#pragma unroll
+                        for (int i = 0; i < W; ++i)
+                            ties += z[i] == z_token && i < to;
+                    }
+                }
+                if (!unit) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        z[i] = scale_logit(z[i], inv_t);
+                }
+                add_up(z, top);
+                most = max3(most, top, top);
             }
-        }
-        if constexpr (TOP) {
-            if (g == g0) {
-                const int held = g1 - g0;
-                const int order = bar_of<T, DT == kBF16 ? 16 : 32>(Row::order_of(best), a.keep, held < T ? held : T, bars);
-                bar_z = fmaxf(kNegMax, Row::from_order(order));
-                collect_edge(most);
-            }
-            if (best >= bar_z)
-                collect(q, top, g);
-            // Segments of 1, 1, 2, 4, .. steps: each doubles what has been seen, and lets
-            // about keep new keys through.
-            if (g + kStep >= segment_end || g + kStep >= g1) {
+            sum.s += static_cast<double>(s_group);
+            sum.t += static_cast<double>(t_group);
+            s_group = t_group = 0.0f;
+            // Segments of 1, 3, 12, 48, .. steps: each makes four times of what has been seen,
+            // and lets about 3 keep new keys through.
+            if (TOP && (g + kStep >= segment_end || g + kStep >= g1)) {
                 close(segment, min(segment_end, g1));
-                segment_end += segment_end - g0;
+                segment_end += 3 * (segment_end - g0);
                 segment = g + kStep;
             }
         }
-        most = max3(most, best, best);
+        if (TOP && g0 == g1)  // a row of no whole group, or a part behind the row's end
+            close(g0, g0);
+    };
+    const uint64_t* list = nullptr;
+    int n = 0;
+    if constexpr (TOP) {
+        Select sel(select_lds, a.keep);
+        body(sel);
+        sel.sort();
+        n = sel.held;
+        list = select_lds.lists[sel.cur];
+    } else {
+        int none = 0;
+        body(none);
     }
-    if (TOP && g0 == g1) {  // a row of no whole group, or a part behind the row's end
-        __syncthreads();
-        collect_edge(most);
-        sel.close();
-    }
-    const Part p = join_threads<T>(most * inv_t, before, sum, join_lds);
-    const int n = sel.held;
+    const Part p = join_threads<T>(most * inv_t, ties + (lane == 0 ? before : 0), sum, edge_x, join_lds);
     if (splits == 1) {
-        write_row(a, row, p, inv_t, token, z_token, select_lds.list, n);
+        write_row(a, row, p, inv_t, token, z_token, list, n);
         return;
     }
     const long at = row * splits + part;
     if (tid == 0)
         parts[at] = p;
     if (TOP && tid < a.keep)
-        keys[at * a.keep + tid] = tid < n ? select_lds.list[tid] : 0;
+        keys[at * a.keep + tid] = tid < n ? list[tid] : 0;
 }
 
 // A row's parts joined, one workgroup per row.
@@ -505,8 +670,7 @@ template <int DT>
 __global__ __launch_bounds__(kT) void logprobs_merge_kernel(LogprobsArgs a, int splits,
                                                             const Part* __restrict__ parts,
                                                             const uint64_t* __restrict__ keys) {
-    __shared__ SelectionLds select_lds;
-    __shared__ int bars[kT + 1];
+    __shared__ SelectionLds<kT> select_lds;
     __shared__ JoinLds<kT> join_lds;
     const int tid = threadIdx.x;
     const long row = blockIdx.x;
@@ -522,40 +686,40 @@ __global__ __launch_bounds__(kT) void logprobs_merge_kernel(LogprobsArgs a, int 
     const RowGroups<DT> r(row_ptr(a.logits, DT, row, a.vocab), a.vocab);
     const float z_token = token >= 0 && token < a.vocab ? r.at_global(token) : 0.0f;
     float m = -__builtin_huge_valf();
-    Sums sum{m, 0.0, 0.0};
+    Sums sum{m, true, 0.0, 0.0};
     int before = 0;
     for (int i = tid; i < splits; i += kT) {
-        Part x = parts[row * splits + i];
-        m = fmaxf(sum.ref, x.m);
-        move_reference(sum.ref, m, sum.s, sum.t);
-        move_reference(x.m, m, x.s, x.t);
-        sum = Sums{m, sum.s + x.s, sum.t + x.t};
-        before += x.before;
+        const Part p = parts[row * splits + i];
+        Sums x{p.m, true, p.s, p.t};
+        m = fmaxf(m, p.m);
+        move_reference(sum, m, true);
+        move_reference(x, m, true);
+        sum.s += x.s;
+        sum.t += x.t;
+        before += p.before;
     }
-    Selection<kT> sel(select_lds, a.keep);
+    Selection<kT, DT == kBF16 ? 16 : 12> sel(select_lds, a.keep);
     if (a.keep) {
         uint64_t best = own[0];
 #pragma unroll
         for (int i = 1; i < kHeld; ++i)
             best = own[i] > best ? own[i] : best;
-        // the upper half of a key rises with the logit; 0, no key, is the lowest
-        const int bar = bar_of<kT, 32>(static_cast<int>(static_cast<uint32_t>(best >> 32) ^ 0x80000000u), a.keep,
-                                       total < kT ? total : kT, bars);
-        const uint64_t least = static_cast<uint64_t>(static_cast<uint32_t>(bar) ^ 0x80000000u) << 32;
-        do {
+        if (total > kCap / 4)
+            sel.begin(best ? key_logit(best) : kNegMax);
+        sel.close([&]() {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
-                if (own[i] >= sel.bar && own[i] >= least)
-                    sel.put(own[i]);
-            for (int i = tid + kHeld * kT; i < total; i += kT) {
-                const uint64_t key = row_keys[i];
-                if (key >= sel.bar && key >= least)
-                    sel.put(key);
+                if (i * kT < total)
+                    sel.put(own[i] >= sel.bar, own[i], sel.cur);
+            for (int i0 = kHeld * kT; i0 < total; i0 += kT) {
+                const uint64_t key = i0 + tid < total ? row_keys[i0 + tid] : 0;
+                sel.put(key >= sel.bar, key, sel.cur);
             }
-        } while (!sel.close());
+        });
+        sel.sort();
     }
-    const Part p = join_threads<kT>(m, before, sum, join_lds);
-    write_row(a, row, p, inv_t, token, z_token, select_lds.list, sel.held);
+    const Part p = join_threads<kT>(m, before, sum, -__builtin_huge_valf(), join_lds);
+    write_row(a, row, p, inv_t, token, z_token, select_lds.lists[sel.cur], sel.held);
 }
 
 // ---------------------------------------------------------------- backward ---

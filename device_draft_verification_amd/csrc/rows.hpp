@@ -253,6 +253,15 @@ __device__ inline void fill(const RowGroups<DT>& r, char* out, int g0, int g1, b
         store_group<DT>(r, out, g, whole, d);
 }
 
+// The integer order of floats (RowGroups::order_max), and back.
+__device__ inline int order32(float z) {
+    const int x = static_cast<int>(__float_as_uint(z));
+    return x ^ ((x >> 31) & 0x7FFFFFFF);
+}
+__device__ inline float from_order32(int o) {
+    return __uint_as_float(static_cast<uint32_t>(o ^ ((o >> 31) & 0x7FFFFFFF)));
+}
+
 __device__ inline bool is_finite_f32(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 __device__ inline bool is_finite_f64(double x) {
     return ((static_cast<uint64_t>(__double_as_longlong(x)) >> 52) & 0x7FF) != 0x7FF;

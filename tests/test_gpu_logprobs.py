@@ -148,13 +148,14 @@ def test_any_alignment(dtype, offset):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("N", [2, 1030])
-@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "two levels", "zeros", "late", "sparse"])
+@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "two levels", "zeros", "denormals", "late", "sparse"])
 def test_orders_that_crowd_the_lists(kind, N, dtype):
     V, K = 18001, 64
     v = torch.arange(V, dtype=torch.float32)
     z = dict(equal=torch.full((V,), 3.0), rising=v / 1000, falling=-v / 1000,
              zeros=torch.where(v % 3 == 1, -0.0, 0.0), late=torch.where(v >= V - 700, 5.0, -5.0) + v / 40000,
              sparse=torch.where(v % 997 == 0, v / V, -float("inf")))
+    z["denormals"] = torch.tensor([-1e-45, -0.0, 0.0, 1e-45, -3e-45])[(v % 5).long()]   # -0 and +0 are one logit
     z["two levels"] = torch.where(v % 5 == 2, 1.0, 0.0)
     z = z[kind].repeat(N, 1).to(DTYPE[dtype]).cuda()
     token = (torch.arange(N, device="cuda", dtype=torch.int32) * 7919) % V
