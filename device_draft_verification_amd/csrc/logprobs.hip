@@ -16,6 +16,7 @@
 #include <new>
 #include <type_traits>
 
+#include "lanes.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
 #include "select.hpp"
@@ -64,22 +65,35 @@ __device__ inline float logit_at_least(uint32_t upper) {
 }
 
 // The k-th largest of 64 N numbers, N in each lane (of the first n chunks), the same
-// in every lane, with the bits below LOW zero: its bits from the top, each by as many
-// ballots as there are chunks.
+// in every lane, with the bits below LOW zero, or `least` if that is larger: its
+// bits from the first in which the largest differs from `least`, two by three
+// ballots a chunk.
 template <int N, int LOW>
-__device__ inline uint32_t kth_largest(const uint32_t (&v)[N], int n, int k) {
-    uint32_t t = 0;
+__device__ inline uint32_t kth_largest(const uint32_t (&v)[N], int n, int k, uint32_t least) {
+    static_assert(LOW % 2 == 0, "bits go in pairs");
+    uint32_t most = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        most = max(most, v[i]);
+    most = __builtin_amdgcn_readfirstlane(over_lanes(most, [](uint32_t a, uint32_t b) { return max(a, b); }));
+    if (most <= least)
+        return least;
+    int bit = (31 - __builtin_clz(most ^ least)) & ~1;
+    uint32_t t = most & ~(static_cast<uint32_t>((4ull << bit) - 1));
 #pragma unroll 1
-    for (int bit = 31; bit >= LOW; --bit) {
-        const uint32_t up = t | 1u << bit;
-        int reach = 0;
+    for (; bit >= LOW; bit -= 2) {
+        const uint32_t one = t | 1u << bit, two = t | 2u << bit, three = t | 3u << bit;
+        int reach1 = 0, reach2 = 0, reach3 = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < n)
-                reach += __popcll(__ballot(v[i] >= up));
-        t = reach >= k ? up : t;
+            if (i < n) {
+                reach1 += __popcll(__ballot(v[i] >= one));
+                reach2 += __popcll(__ballot(v[i] >= two));
+                reach3 += __popcll(__ballot(v[i] >= three));
+            }
+        t = reach3 >= k ? three : reach2 >= k ? two : reach1 >= k ? one : t;
     }
-    return t;
+    return max(t, least);
 }
 
 // A row's first entries, gathered over segments of it. While a segment goes by,
@@ -96,7 +110,7 @@ struct SelectionLds {
     uint64_t bar;
     int counts[2];     // keys put into the lists, also those that one had no place for
     int lost;          // groups that a wavefront had no place for
-    uint32_t most[T];  // the threads' largest entries
+    uint32_t bars[T / 64];  // the wavefronts' first ones
 };
 
 template <int T, int G>
@@ -120,28 +134,43 @@ struct Selection {
         lds_barrier();
     }
 
-    // Each lane's key, where it has one, into list `to`; the whole wavefront calls it.
-    __device__ void put(bool has, uint64_t key, int to) {
-        const uint64_t mask = __ballot(has);
-        if (mask == 0)
+    // Each lane's keys, where it has them, into list `to`; the whole wavefront calls it.
+    template <int N>
+    __device__ void put(const bool (&has)[N], const uint64_t (&key)[N], int to) {
+        uint64_t mask[N];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            mask[i] = __ballot(has[i]);
+            n += __popcll(mask[i]);
+        }
+        if (n == 0)
             return;
         int base = 0;
         if ((threadIdx.x & 63) == 0)
-            base = atomicAdd(&lds.counts[to], __popcll(mask));
-        const int slot = __builtin_amdgcn_readfirstlane(base) + lanes_below(mask);
-        if (has && slot < kCap)
-            lds.lists[to][slot] = key;
+            base = atomicAdd(&lds.counts[to], n);
+        base = __builtin_amdgcn_readfirstlane(base);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int slot = base + lanes_below(mask[i]);
+            if (has[i] && slot < kCap)
+                lds.lists[to][slot] = key[i];
+            base += __popcll(mask[i]);
+        }
     }
 
-    // A first bar: that of the threads' largest entries.
+    // A first bar: every wavefront has its share of keep threads whose largest entry
+    // reaches it.
     __device__ void begin(float most) {
-        lds.most[threadIdx.x] = ordered32(most + 0.0f);
+        const uint32_t v[1] = {ordered32(most + 0.0f)};
+        const uint32_t mine = kth_largest<1, LOW>(v, 1, (keep + T / 64 - 1) / (T / 64), 0u);
+        lds.bars[threadIdx.x >> 6] = mine;
         lds_barrier();
-        uint32_t v[T / 64];
+        uint32_t b = lds.bars[0];
 #pragma unroll
-        for (int i = 0; i < T / 64; ++i)
-            v[i] = lds.most[threadIdx.x % 64 + 64 * i];
-        raise(static_cast<uint64_t>(kth_largest<T / 64, LOW>(v, T / 64, keep)) << 32);
+        for (int w = 1; w < T / 64; ++w)
+            b = min(b, lds.bars[w]);
+        raise(static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(b))) << 32);
     }
 
     __device__ void raise(uint64_t to) { bar = to > bar ? to : bar; }
@@ -193,11 +222,14 @@ struct Selection {
             key[i] = i < chunks && 64 * i + lane < held ? lds.lists[cur][64 * i + lane] : 0;
             v[i] = static_cast<uint32_t>(key[i] >> 32);
         }
-        raise(static_cast<uint64_t>(kth_largest<N, LOW>(v, chunks, keep)) << 32);
+        raise(static_cast<uint64_t>(kth_largest<N, LOW>(v, chunks, keep, static_cast<uint32_t>(bar >> 32))) << 32);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < chunks && i % (T / 64) == static_cast<int>(threadIdx.x >> 6))
-                put(key[i] >= bar, key[i], cur ^ 1);
+            if (i < chunks && i % (T / 64) == static_cast<int>(threadIdx.x >> 6)) {
+                const bool has[1] = {key[i] >= bar};
+                const uint64_t one[1] = {key[i]};
+                put(has, one, cur ^ 1);
+            }
         swap();
     }
 
@@ -228,16 +260,15 @@ struct Selection {
             if ((at & ~63) >= n)
                 continue;  // wavefronts without a key have nothing to rank
             const uint64_t mine = at < n ? list[at] : ~0ull;
-            int larger = 0, j = 0;
-            for (; j + 16 <= n; j += 16)
+            int larger = 0;
+#pragma unroll 1
+            for (int j = 0; j < n; j += 16)  // what lies behind the n keys does not count
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
                     const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + j + k);
-                    larger += two.x > mine;
-                    larger += two.y > mine;
+                    larger += two.x > mine && j + k < n;
+                    larger += two.y > mine && j + k + 1 < n;
                 }
-            for (; j < n; ++j)
-                larger += list[j] > mine;
             if (at < n && larger < keep) {
                 lds.lists[cur ^ 1][larger] = mine;
                 if (larger == keep - 1)
@@ -333,7 +364,7 @@ struct JoinLds {
 template <int T>
 __device__ inline Part join_threads(float m, int before, Sums x, float edge_x, JoinLds<T>& lds) {
     const int wid = threadIdx.x >> 6;
-    m = wave_max(m);
+    m = over_lanes(m, [](float a, float b) { return fmaxf(a, b); });
     if ((threadIdx.x & 63) == 0)
         lds.m[wid] = m;
     lds_barrier();
@@ -346,11 +377,10 @@ __device__ inline Part join_threads(float m, int before, Sums x, float edge_x, J
         x.s += static_cast<double>(e);
         x.t += static_cast<double>(e * fmaxf(d, kNegMax));
     }
-    x.s = wave_sum(x.s);
-    x.t = wave_sum(x.t);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-        before += __shfl_xor(before, off, 64);
+    auto sum = [](auto a, auto b) { return a + b; };
+    x.s = over_lanes(x.s, sum);
+    x.t = over_lanes(x.t, sum);
+    before = over_lanes(before, sum);
     if ((threadIdx.x & 63) == 0) {
         lds.before[wid] = before;
         lds.s[wid] = x.s;
@@ -391,7 +421,7 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
         }
         a.out_logprob[row] = bad ? nan : lp;
         a.out_rank[row] = bad ? -1 : rank;
-        a.out_entropy[row] = bad ? nan : empty ? 0.0f : fmaxf(static_cast<float>(log_s - p.t / p.s / static_cast<double>(kLog2e)), 0.0f);
+        a.out_entropy[row] = bad ? nan : empty ? 0.0f : fmaxf(static_cast<float>(log_s - p.t / p.s * (1.0 / static_cast<double>(kLog2e))), 0.0f);
         a.out_norm[2 * row] = bad ? nan : p.m;
         a.out_norm[2 * row + 1] = bad ? nan : static_cast<float>(log_s);
     }
@@ -412,7 +442,7 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
 }
 
 template <int DT, int T, int U, bool TOP>
-__global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits, int per_split,
+__global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int splits, int per_split,
                                                      Part* __restrict__ parts, uint64_t* __restrict__ keys) {
     using Row = RowGroups<DT>;
     constexpr int W = Row::W;
@@ -511,7 +541,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits,
                     holes = true;
                     continue;
                 }
-                const float best = uniform(wave_max(max3(most, top, top)) * inv_t);
+                const float best = uniform(over_lanes(max3(most, top, top), [](float a, float b) { return max3(a, b, b); }) * inv_t);
                 if (best > ref_x) {
                     ref_x = best;
                     sum.s += static_cast<double>(s_group);
@@ -542,6 +572,23 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits,
         }
     };
 
+    // Of the first step's groups, which are all put aside, those that reach the bar.
+    auto narrow_aside = [&]() {
+        if constexpr (TOP) {
+            const int n = put_aside;
+            put_aside = 0;
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += 64) {
+                const int i = min(i0 + lane, kAside - 1);
+                const uint4 x = aside.data[wid][i];
+                const int at = aside.at[wid][i];
+                float z[W];
+                Row::unpack(x, z);
+                collect(x, i0 + lane < n ? largest(z) : -inf, at);  // to a place at or before its own
+            }
+        }
+    };
+
     auto body = [&](auto& sel) {
         // Ends the segment [from, to). If it had more groups than there is place for, its
         // steps are gone through again, from memory, each as a segment.
@@ -550,25 +597,41 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits,
                 auto end = [&](bool first) {
                     if (put_aside > kAside)
                         select_lds.lost = 1;
-                    if (first)
+                    if (first) {
                         sel.begin(most);
+                        bar_z = logit_at_least(static_cast<uint32_t>(sel.bar >> 32));
+                        narrow_aside();
+                    }
                     const bool done = sel.close([&]() {
+                        // Lane by lane the next entry that reaches the bar: most groups have one.
+                        const int n = min(put_aside, kAside);
 #pragma unroll 1
-                        for (int i0 = 0; i0 < min(put_aside, kAside); i0 += 64) {
-                            const int i = i0 + lane;
-                            const bool mine = i < min(put_aside, kAside);
+                        for (int i0 = 0; i0 < n; i0 += 64) {
+                            const int i = min(i0 + lane, kAside - 1);
                             float z[W];
-                            Row::unpack(mine ? aside.data[wid][i] : Row::neg_inf(), z);
-                            const int v0 = mine ? static_cast<int>(r.element(aside.at[wid][i])) : 0;
+                            Row::unpack(aside.data[wid][i], z);
+                            const int v0 = static_cast<int>(r.element(aside.at[wid][i]));
+                            unsigned hits = 0;
 #pragma unroll
-                            for (int e = 0; e < W; ++e) {
-                                const uint64_t key = make_key(z[e], v0 + e);
-                                sel.put(z[e] >= kNegMax && key >= sel.bar, key, sel.cur);
+                            for (int e = 0; e < W; ++e)
+                                hits |= z[e] >= bar_z ? 1u << e : 0u;
+                            hits = i0 + lane < n ? hits : 0u;
+                            while (__ballot(hits != 0)) {
+                                const int e = __builtin_ctz(hits | 1u << W);
+                                float y = z[0];
+#pragma unroll
+                                for (int k = 1; k < W; ++k)
+                                    y = e == k ? z[k] : y;
+                                const uint64_t key[1] = {make_key(y, v0 + e)};
+                                const bool has[1] = {hits != 0 && key[0] >= sel.bar};
+                                sel.put(has, key, sel.cur);
+                                hits &= hits - 1;
                             }
                         }
                         if (first) {
-                            const uint64_t key = make_key(edge_z, edge);
-                            sel.put(edge_z >= kNegMax && key >= sel.bar, key, sel.cur);
+                            const uint64_t key[1] = {make_key(edge_z, edge)};
+                            const bool has[1] = {edge_z >= kNegMax && key[0] >= sel.bar};
+                            sel.put(has, key, sel.cur);
                         }
                     });
                     put_aside = 0;
@@ -587,7 +650,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, int splits,
                         Row::unpack(x, z);
                         collect(x, largest(z), at);
                     }
-                    end(g == g0);
+                    end(false);
                 }
             }
         };
@@ -707,13 +770,15 @@ __global__ __launch_bounds__(kT) void logprobs_merge_kernel(LogprobsArgs a, int 
         if (total > kCap / 4)
             sel.begin(best ? key_logit(best) : kNegMax);
         sel.close([&]() {
+            bool has[kHeld];
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
-                if (i * kT < total)
-                    sel.put(own[i] >= sel.bar, own[i], sel.cur);
+                has[i] = own[i] >= sel.bar;
+            sel.put(has, own, sel.cur);
             for (int i0 = kHeld * kT; i0 < total; i0 += kT) {
-                const uint64_t key = i0 + tid < total ? row_keys[i0 + tid] : 0;
-                sel.put(key >= sel.bar, key, sel.cur);
+                const uint64_t key[1] = {i0 + tid < total ? row_keys[i0 + tid] : 0};
+                const bool one[1] = {key[0] >= sel.bar};
+                sel.put(one, key, sel.cur);
             }
         });
         sel.sort();
