@@ -163,7 +163,9 @@ struct Selection {
     // reaches it.
     __device__ void begin(float most) {
         const uint32_t v[1] = {ordered32(most + 0.0f)};
-        const uint32_t mine = kth_largest<1, LOW>(v, 1, (keep + T / 64 - 1) / (T / 64), 0u);
+        const uint32_t least = over_lanes(v[0], [](uint32_t a, uint32_t b) { return min(a, b); });
+        const uint32_t mine = kth_largest<1, LOW>(v, 1, (keep + T / 64 - 1) / (T / 64),
+                                                  __builtin_amdgcn_readfirstlane(least));
         lds.bars[threadIdx.x >> 6] = mine;
         lds_barrier();
         uint32_t b = lds.bars[0];
@@ -179,7 +181,7 @@ struct Selection {
     // that are at least the bar into list `cur`. False: groups were lost, and nothing
     // has changed.
     template <typename F>
-    __device__ bool close(F&& f) {
+    __device__ bool close(bool last, F&& f) {
         int n;
         for (;;) {
             f();
@@ -204,9 +206,10 @@ struct Selection {
                 return false;
         }
         held = n;
-        if (n > keep + 16)
+        // Before the last ranking more keys are cheaper than a narrower list.
+        if (n > (last ? 3 * keep : keep + 16))
             narrow();
-        if (held > keep + 64)  // that many are equal
+        if (!last && held > keep + 64)  // that many are equal
             sort();
         return true;
     }
@@ -251,25 +254,25 @@ struct Selection {
             lds.counts[cur ^ 1] = 0;  // seen by all behind the next barrier, before its next use
     }
 
-    // The keep largest of the list's first n keys, largest first, into the other list.
+    // The keep largest of the list's first n keys, largest first, into the other list:
+    // four lanes to a key, each compares it with a quarter of the list.
     __device__ void rank(int n) const {
         const uint64_t* list = lds.lists[cur];
-#pragma unroll
-        for (int i = 0; i < (kCap + T - 1) / T; ++i) {
-            const int at = static_cast<int>(threadIdx.x) + i * T;
-            if ((at & ~63) >= n)
-                continue;  // wavefronts without a key have nothing to rank
-            const uint64_t mine = at < n ? list[at] : ~0ull;
-            int larger = 0;
+        const int quarter = static_cast<int>(threadIdx.x) & 3;
 #pragma unroll 1
-            for (int j = 0; j < n; j += 16)  // what lies behind the n keys does not count
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + j + k);
-                    larger += two.x > mine && j + k < n;
-                    larger += two.y > mine && j + k + 1 < n;
-                }
-            if (at < n && larger < keep) {
+        for (int i = static_cast<int>(threadIdx.x) >> 2; (i & ~15) < n; i += T / 4) {
+            const uint64_t mine = i < n ? list[i] : ~0ull;
+            int larger = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; j += 8) {  // what lies behind the n keys does not count
+                const int at = j + 2 * quarter;
+                const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(list + at);
+                larger += two.x > mine && at < n;
+                larger += two.y > mine && at + 1 < n;
+            }
+            larger += lane_move<0xB1>(larger);
+            larger += lane_move<0x4E>(larger);
+            if (quarter == 0 && i < n && larger < keep) {
                 lds.lists[cur ^ 1][larger] = mine;
                 if (larger == keep - 1)
                     lds.bar = mine;
@@ -594,7 +597,7 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
         // steps are gone through again, from memory, each as a segment.
         auto close = [&](int from, int to) {
             if constexpr (TOP) {
-                auto end = [&](bool first) {
+                auto end = [&](bool first, bool last) {
                     if (put_aside > kAside)
                         select_lds.lost = 1;
                     if (first) {
@@ -602,7 +605,7 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
                         bar_z = logit_at_least(static_cast<uint32_t>(sel.bar >> 32));
                         narrow_aside();
                     }
-                    const bool done = sel.close([&]() {
+                    const bool done = sel.close(last, [&]() {
                         // Lane by lane the next entry that reaches the bar: most groups have one.
                         const int n = min(put_aside, kAside);
 #pragma unroll 1
@@ -638,7 +641,7 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
                     bar_z = logit_at_least(static_cast<uint32_t>(sel.bar >> 32));
                     return done;
                 };
-                if (end(from == g0))
+                if (end(from == g0, to == g1))
                     return;
 #pragma unroll 1
                 for (int g = from; g < to; g += kStep) {
@@ -650,7 +653,7 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
                         Row::unpack(x, z);
                         collect(x, largest(z), at);
                     }
-                    end(false);
+                    end(false, g + kStep >= g1);
                 }
             }
         };
@@ -769,7 +772,7 @@ __global__ __launch_bounds__(kT) void logprobs_merge_kernel(LogprobsArgs a, int 
             best = own[i] > best ? own[i] : best;
         if (total > kCap / 4)
             sel.begin(best ? key_logit(best) : kNegMax);
-        sel.close([&]() {
+        sel.close(true, [&]() {
             bool has[kHeld];
 #pragma unroll
             for (int i = 0; i < kHeld; ++i)
