@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.hpp"
 #include "spec_mxfp4.h"
@@ -213,6 +214,16 @@ __global__ __launch_bounds__(kBlock) void mxfp4_quantize_kernel(const void* x, i
 // and scales past the depth come from a page of zeros.
 __device__ int4 zero_chunk;  // zero from load on, never written
 
+// SIZE bytes a lane from memory into LDS, behind one another there.
+template <int SIZE>
+__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* to) {
+    static_assert(SIZE == 16 || SIZE == 4, "of the sizes that the loads know");
+    if constexpr (SIZE == 16)
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from), to, 16, 0, 0);
+    else
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from), to, 4, 0, 0);
+}
+
 template <int BYTE>
 __device__ __forceinline__ f32x16 multiply_blocks(const i32x4& a, const i32x4& b, const f32x16& c, int sa, int sb) {
     const i32x8 x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -221,7 +232,7 @@ __device__ __forceinline__ f32x16 multiply_blocks(const i32x4& a, const i32x4& b
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
-template <int TV, int TN, int WV, int WN, int BK, int RING, int OUT>
+template <int TV, int TN, int WV, int WN, int BK, int OUT>
 __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_scale, const uint8_t* __restrict__ w,
     const uint8_t* __restrict__ w_scale, int rows, int depth, int cols, int tiles_n, int tiles,
@@ -229,22 +240,29 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     constexpr int kWavesHere = WV * WN;
     constexpr int MV = TV / WV / 32, MN = TN / WN / 32;
     constexpr int kRows = TV + TN;
-    constexpr int kWords = BK / 64;                   // of a row's scales in a slot
-    constexpr int kSlot = kRows * (BK + 4 * kWords);
     constexpr int kChunks = BK / 16;                  // of a row in a slot
     constexpr int kRowsPerLoad = 64 / kChunks;        // a load covers 1 KiB
-    constexpr int kLoads = kRows * BK / 1024 / kWavesHere;  // per wavefront and stage
-    constexpr int kScaleLoads = (kRows * kWords / 64 + kWavesHere - 1) / kWavesHere;
+    constexpr int kLoads = kRows / kRowsPerLoad / kWavesHere;  // per wavefront and stage
+    constexpr int kLoadsV = TV / kRowsPerLoad / kWavesHere;    // of them of the vocabulary
+    constexpr int kWords = BK / 64;                   // of a row's scales of a stage
+    constexpr int kPeriod = 4;                        // stages whose scales are loaded together
+    constexpr int kRowWords = kWords * kPeriod;       // of a row's scales in LDS
+    constexpr int kScaleLoads = kLoads / kPeriod;     // per wavefront and stage
+    constexpr int kSlot = kRows * BK;
+    constexpr int kScaleSlot = kRows * 4 * kRowWords;
+    constexpr int kRing = 2 * kSlot;
     constexpr int kSteps = BK / 32;                   // of two blocks each
-    static_assert(kRows * BK / 1024 % kWavesHere == 0, "every wavefront issues the same loads");
-    static_assert(kRows * kWords % 64 == 0, "whole loads of scales");
-    static_assert(kSteps % 2 == 0 && kSteps / 4 * 2 == kWords, "two sets of fragments take turns");
-    auto swizzle = [](int row) { return (BK <= 256 ? row / (256 / BK) : row) % kChunks; };
+    static_assert(TV % (kRowsPerLoad * kWavesHere) == 0 && TN % (kRowsPerLoad * kWavesHere) == 0 &&
+                      kLoads % kPeriod == 0, "every wavefront issues the same loads");
+    static_assert(kRowWords == kChunks, "a load of scales covers the rows that one of codes does");
+    static_assert(kSteps % 4 == 0 && 256 % BK == 0 && kWavesHere * kRowsPerLoad % (256 / BK * kChunks) == 0,
+                  "two sets of fragments take turns, and a lane's place in its row is the same in all loads");
+    auto swizzle = [](int row) { return row / (256 / BK) % kChunks; };
     // The epilogue turns a wavefront's 32 rows x 32 MV entries through LDS.
     constexpr int ESZ = OUT == kBF16 ? 2 : 4;
     constexpr int kRowBytes = 32 * MV * ESZ + 16;
     constexpr int kTurn = 32 * kRowBytes;
-    constexpr int kLds = RING * kSlot > kWavesHere * kTurn ? RING * kSlot : kWavesHere * kTurn;
+    constexpr int kLds = kRing + 2 * kScaleSlot > kWavesHere * kTurn ? kRing + 2 * kScaleSlot : kWavesHere * kTurn;
     __shared__ __align__(16) uint8_t lds[kLds];
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
@@ -257,50 +275,43 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     const int n0 = tile % tiles_n * TN;
     const int bytes = depth / 2, words = depth / 128;  // of a row: codes, words of scales
 
-    // This lane's chunk of each of its wavefront's loads, and its word of scales.
-    auto row_of = [&](int row, const uint8_t* of_w, const uint8_t* of_a, int stride) {
-        if (row < TV) {
-            const int v = v0 + row;
-            return of_w + static_cast<size_t>(v < cols ? v : cols - 1) * stride;
-        }
-        const int n = n0 + row - TV;
-        return of_a + static_cast<size_t>(n < rows ? n : rows - 1) * stride;
-    };
-    const uint8_t* src[kLoads];
-    int chunk[kLoads];
+    // Load i of a wavefront covers rows kRowsPerLoad * (wavefront + kWavesHere * i) and
+    // on: of each this lane's row, as an offset from the tile's first (the scales' is
+    // a sixteenth), and its chunk and word in it.
+    const uint8_t* w_tile = w + static_cast<size_t>(v0) * bytes;
+    const uint8_t* a_tile = a + static_cast<size_t>(n0) * bytes;
+    const uint8_t* w_scale_tile = w_scale + static_cast<size_t>(v0) * (bytes / 16);
+    const uint8_t* a_scale_tile = a_scale + static_cast<size_t>(n0) * (bytes / 16);
+    const int first_row = wid * kRowsPerLoad + lane / kChunks;
+    const uint32_t chunk = (lane % kChunks ^ swizzle(first_row)) * 16, word = lane % kRowWords;
+    uint32_t row_at[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int row = (wid + kWavesHere * i) * kRowsPerLoad + lane / kChunks;
-        chunk[i] = (lane % kChunks ^ swizzle(row)) * 16;
-        src[i] = row_of(row, w, a, bytes) + chunk[i];
-    }
-    // Wavefronts past the last load of scales repeat an earlier one.
-    constexpr int kAll = kRows * kWords / 64;
-    const uint8_t* scale_src[kScaleLoads];
-    int scale_to[kScaleLoads];
-    const int word = lane % kWords;
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-        const int load = (wid + kWavesHere * i) % kAll;
-        scale_src[i] = row_of(load * (64 / kWords) + lane / kWords, w_scale, a_scale, words * 4) + 4 * word;
-        scale_to[i] = kRows * BK + load * 256;
+        const int row = first_row + kRowsPerLoad * kWavesHere * i;
+        row_at[i] = static_cast<uint32_t>(i < kLoadsV ? min(row, cols - 1 - v0) : min(row - TV, rows - 1 - n0)) * bytes;
     }
     const int stages = (bytes + BK - 1) / BK;
     const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero_chunk);
     asm volatile("" : "+s"(zeros));  // looked up once, not in every stage
+    // Stages and periods past the end load zeros into places that nobody reads.
     auto issue = [&](int s, int i) {
-        uint8_t* slot = lds + (s % RING) * kSlot;
-        // stages past the end load zeros into slots that nobody reads
-        if (i < kLoads) {
-            const int k = s * BK;
-            const uint8_t* from = k + BK <= bytes || k + chunk[i] < bytes ? src[i] + k : zeros;
-            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from),
-                                             slot + (wid + kWavesHere * i) * 1024, 16, 0, 0);
-        } else {
-            const int k = s * kWords;
-            const uint8_t* from = k + kWords <= words || k + word < words ? scale_src[i - kLoads] + 4 * k : zeros;
-            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(from), slot + scale_to[i - kLoads], 4, 0, 0);
-        }
+        const int k = s * BK;
+        const uint8_t* tile = (i < kLoadsV ? w_tile : a_tile) + k;
+        uint8_t* to = lds + (s & 1) * kSlot + (wid + kWavesHere * i) * 1024;
+        if (k + BK <= bytes)
+            to_lds<16>(tile + (row_at[i] + chunk), to);
+        else
+            to_lds<16>(k + static_cast<int>(chunk) < bytes ? tile + (row_at[i] + chunk) : zeros, to);
+    };
+    // Load i of a period's scales.
+    auto issue_scales = [&](int p, int i) {
+        const int k = p * kRowWords;
+        const uint8_t* tile = (i < kLoadsV ? w_scale_tile : a_scale_tile) + 4 * k;
+        uint8_t* to = lds + kRing + (p & 1) * kScaleSlot + (wid + kWavesHere * i) * 256;
+        if (k + kRowWords <= words)
+            to_lds<4>(tile + (row_at[i] / 16 + 4 * word), to);
+        else
+            to_lds<4>(k + static_cast<int>(word) < words ? tile + (row_at[i] / 16 + 4 * word) : zeros, to);
     };
     constexpr int kIssues = kLoads + kScaleLoads;
     f32x16 acc[MV][MN];
@@ -310,10 +321,10 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
         for (int j = 0; j < MN; ++j)
             acc[i][j] = f32x16{};
 #pragma unroll
-    for (int s = 0; s < RING - 1; ++s)
-#pragma unroll
-        for (int i = 0; i < kIssues; ++i)
-            issue(s, i);
+    for (int i = 0; i < kLoads; ++i) {
+        issue_scales(0, i);
+        issue(0, i);
+    }
     const int wv = wid % WV * (TV / WV), wn = wid / WV * (TN / WN);
     const int frag_row = lane & 31, half = lane >> 5;
     const int swz = swizzle(frag_row);  // rows of a tile start at multiples of 32
@@ -326,7 +337,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     i32x4 fw[2][MV], fa[2][MN];
     int sw[2][kHalfWords][MV], sa[2][kHalfWords][MN];  // of this stage, and of the one before
     auto read = [&](int s, int step, int i) {
-        const uint8_t* slot = lds + (s % RING) * kSlot;
+        const uint8_t* slot = lds + (s & 1) * kSlot;
         const int pos = ((half * kSteps + step) ^ swz) * 16;
         if (i < MN)
             fa[step & 1][i] = *reinterpret_cast<const i32x4*>(slot + (TV + wn + 32 * i + frag_row) * BK + pos);
@@ -335,11 +346,11 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                 *reinterpret_cast<const i32x4*>(slot + (wv + 32 * (i - MN) + frag_row) * BK + pos);
     };
     auto read_scales = [&](int s, int i) {
-        const int* scales = reinterpret_cast<const int*>(lds + (s % RING) * kSlot + kRows * BK);
+        const int* scales = reinterpret_cast<const int*>(lds + kRing + (s / kPeriod & 1) * kScaleSlot);
         const int row = i < MN ? TV + wn + 32 * i + frag_row : wv + 32 * (i - MN) + frag_row;
 #pragma unroll
         for (int h = 0; h < kHalfWords; ++h) {
-            const int v = scales[row * kWords + half * kHalfWords + h];
+            const int v = scales[row * kRowWords + s % kPeriod * kWords + half * kHalfWords + h];
             if (i < MN)
                 sa[0][h][i] = v;
             else
@@ -360,10 +371,16 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     };
     // Of `work` pieces spread over `steps` steps, the first of step n.
     auto share = [](int n, int steps, int work) { return (n * work + steps - 1) / steps; };
-    for (int s = 0; s < stages; ++s) {
-        // Stage s has landed once at most the RING - 2 stages after it are out;
-        // past the barrier every wavefront has also read all of stage s - 1.
-        stage_barrier<kIssues*(RING - 2)>();
+#pragma unroll 1
+    for (int s0 = 0; s0 < stages; s0 += kPeriod)
+#pragma unroll
+    for (int j = 0; j < kPeriod; ++j) {
+        const int s = s0 + j;
+        if (s >= stages)
+            break;
+        // Stage s has landed; past the barrier every wavefront has also read all of
+        // stage s - 1.
+        stage_barrier<0>();
 #pragma unroll
         for (int h = 0; h < kHalfWords; ++h) {
 #pragma unroll
@@ -388,8 +405,10 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                         read(s, h, p);
                     else if (p < 2 * kReads)
                         read_scales(s, p - kReads);
+                    else if (p < 2 * kReads + kLoads)
+                        issue(s + 1, p - 2 * kReads);
                     else
-                        issue(s + RING - 1, p - 2 * kReads);
+                        issue_scales(s / kPeriod + 1, p - 2 * kReads - kLoads + kScaleLoads * j);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -456,7 +475,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     }
 }
 
-template <int TV, int TN, int WV, int WN, int BK, int RING>
+template <int TV, int TN, int WV, int WN, int BK>
 hipError_t launch_tile(int rows, int depth, int cols, const uint8_t* a, const uint8_t* a_scale,
                        const uint8_t* w, const uint8_t* w_scale, int out_dtype, void* out, hipStream_t s) {
     const long tiles_v = (static_cast<long>(cols) + TV - 1) / TV;
@@ -465,11 +484,11 @@ hipError_t launch_tile(int rows, int depth, int cols, const uint8_t* a, const ui
         return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(tiles_v * tiles_n)), block(64 * WV * WN);
     if (out_dtype == SPEC_BF16)
-        mxfp4_product_kernel<TV, TN, WV, WN, BK, RING, kBF16><<<grid, block, 0, s>>>(
+        mxfp4_product_kernel<TV, TN, WV, WN, BK, kBF16><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     else
-        mxfp4_product_kernel<TV, TN, WV, WN, BK, RING, kF32><<<grid, block, 0, s>>>(
+        mxfp4_product_kernel<TV, TN, WV, WN, BK, kF32><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     return hipGetLastError();
@@ -540,11 +559,11 @@ int spec_mxfp4_product(int rows, int depth, int cols, const uint8_t* a, const ui
 #define SPEC_TILE(...) \
     e = launch_tile<__VA_ARGS__>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s)
     if (rows > 128 && tiles(256, 256) >= 224)
-        SPEC_TILE(256, 256, 2, 4, 128, 2);
+        SPEC_TILE(256, 256, 2, 4, 128);
     else if (rows > 64 && tiles(128, 128) >= 448)
-        SPEC_TILE(128, 128, 2, 2, 128, 2);
+        SPEC_TILE(128, 128, 2, 2, 128);
     else
-        SPEC_TILE(64, 32, 2, 1, 128, 3);
+        SPEC_TILE(64, 64, 2, 1, 128);
 #undef SPEC_TILE
     return e == hipSuccess ? SPEC_OK : e == hipErrorInvalidValue ? SPEC_EINVAL : SPEC_EHIP;
 }
