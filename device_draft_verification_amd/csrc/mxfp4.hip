@@ -5,6 +5,7 @@
 //   out[n][v] = sum_b 2^(ea + ew) sum_{k in block b} a[n][k] w[v][k].
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -232,7 +233,7 @@ __device__ __forceinline__ f32x16 multiply_blocks(const i32x4& a, const i32x4& b
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
-template <int TV, int TN, int WV, int WN, int BK, int OUT>
+template <int TV, int TN, int WV, int WN, int OUT>
 __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_scale, const uint8_t* __restrict__ w,
     const uint8_t* __restrict__ w_scale, int rows, int depth, int cols, int tiles_n, int tiles,
@@ -240,129 +241,117 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     constexpr int kWavesHere = WV * WN;
     constexpr int MV = TV / WV / 32, MN = TN / WN / 32;
     constexpr int kRows = TV + TN;
-    constexpr int kChunks = BK / 16;                  // of a row in a slot
-    constexpr int kRowsPerLoad = 64 / kChunks;        // a load covers 1 KiB
-    constexpr int kLoads = kRows / kRowsPerLoad / kWavesHere;  // per wavefront and stage
-    constexpr int kLoadsV = TV / kRowsPerLoad / kWavesHere;    // of them of the vocabulary
-    constexpr int kWords = BK / 64;                   // of a row's scales of a stage
-    constexpr int kPeriod = 4;                        // stages whose scales are loaded together
-    constexpr int kRowWords = kWords * kPeriod;       // of a row's scales in LDS
+    constexpr int BK = 128;                           // bytes of a row's codes in a stage
+    constexpr int kLoads = kRows / 8 / kWavesHere;    // per wavefront and stage: a load covers 8 rows
+    constexpr int kLoadsV = TV / 8 / kWavesHere;      // of them of the vocabulary
+    constexpr int kPeriod = 4;                        // stages whose scales are loaded together: a word
+    constexpr int kRowWords = 2 * kPeriod;            // of scales for 64 bytes of codes
     constexpr int kScaleLoads = kLoads / kPeriod;     // per wavefront and stage
     constexpr int kSlot = kRows * BK;
     constexpr int kScaleSlot = kRows * 4 * kRowWords;
-    constexpr int kRing = 2 * kSlot;
     constexpr int kSteps = BK / 32;                   // of two blocks each
-    static_assert(TV % (kRowsPerLoad * kWavesHere) == 0 && TN % (kRowsPerLoad * kWavesHere) == 0 &&
-                      kLoads % kPeriod == 0, "every wavefront issues the same loads");
-    static_assert(kRowWords == kChunks, "a load of scales covers the rows that one of codes does");
-    static_assert(kSteps % 4 == 0 && 256 % BK == 0 && kWavesHere * kRowsPerLoad % (256 / BK * kChunks) == 0,
-                  "two sets of fragments take turns, and a lane's place in its row is the same in all loads");
-    auto swizzle = [](int row) { return row / (256 / BK) % kChunks; };
-    // The epilogue turns a wavefront's 32 rows x 32 MV entries through LDS.
+    static_assert(TV % (8 * kWavesHere) == 0 && TN % (8 * kWavesHere) == 0 && kLoads % kPeriod == 0,
+                  "every wavefront issues the same loads");
+    static_assert(kWavesHere % 2 == 0, "a lane's chunk is the same in all loads");
+    // The epilogue turns 32 rows x 128 bytes of a wavefront's outputs through LDS at a
+    // time, in the slot of the last stage.
     constexpr int ESZ = OUT == kBF16 ? 2 : 4;
-    constexpr int kRowBytes = 32 * MV * ESZ + 16;
+    constexpr int kTurnV = 128 / ESZ / 32;            // fragments of the vocabulary at a time
+    constexpr int kRowBytes = 128 + 16;
     constexpr int kTurn = 32 * kRowBytes;
-    constexpr int kLds = kRing + 2 * kScaleSlot > kWavesHere * kTurn ? kRing + 2 * kScaleSlot : kWavesHere * kTurn;
-    __shared__ __align__(16) uint8_t lds[kLds];
+    static_assert(MV % kTurnV == 0 && kWavesHere * kTurn <= kSlot, "outputs turn inside a slot");
+    // One LDS object: with two the compiler keeps their accesses apart by alias
+    // scopes, and then waits for every load into LDS before any read of it.
+    __shared__ __align__(16) uint8_t lds[2 * kSlot + 2 * kScaleSlot];
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    // Workgroups go round the eight XCDs: each XCD takes a contiguous run of
-    // tiles, rows fastest, so that the tiles that share weights share an L2.
-    const int blk = blockIdx.x, xcd = blk & 7, order = blk >> 3;
-    const int per = tiles >> 3, extra = tiles & 7;
-    const int tile = xcd * per + (xcd < extra ? xcd : extra) + order;
-    const int v0 = tile / tiles_n * TV;
-    const int n0 = tile % tiles_n * TN;
     const int bytes = depth / 2, words = depth / 128;  // of a row: codes, words of scales
-
-    // Load i of a wavefront covers rows kRowsPerLoad * (wavefront + kWavesHere * i) and
-    // on: of each this lane's row, as an offset from the tile's first (the scales' is
-    // a sixteenth), and its chunk and word in it.
-    const uint8_t* w_tile = w + static_cast<size_t>(v0) * bytes;
-    const uint8_t* a_tile = a + static_cast<size_t>(n0) * bytes;
-    const uint8_t* w_scale_tile = w_scale + static_cast<size_t>(v0) * (bytes / 16);
-    const uint8_t* a_scale_tile = a_scale + static_cast<size_t>(n0) * (bytes / 16);
-    const int first_row = wid * kRowsPerLoad + lane / kChunks;
-    const uint32_t chunk = (lane % kChunks ^ swizzle(first_row)) * 16, word = lane % kRowWords;
-    uint32_t row_at[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int row = first_row + kRowsPerLoad * kWavesHere * i;
-        row_at[i] = static_cast<uint32_t>(i < kLoadsV ? min(row, cols - 1 - v0) : min(row - TV, rows - 1 - n0)) * bytes;
-    }
     const int stages = (bytes + BK - 1) / BK;
-    const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero_chunk);
-    asm volatile("" : "+s"(zeros));  // looked up once, not in every stage
-    // Stages and periods past the end load zeros into places that nobody reads.
-    auto issue = [&](int s, int i) {
-        const int k = s * BK;
-        const uint8_t* tile = (i < kLoadsV ? w_tile : a_tile) + k;
-        uint8_t* to = lds + (s & 1) * kSlot + (wid + kWavesHere * i) * 1024;
-        if (k + BK <= bytes)
-            to_lds<16>(tile + (row_at[i] + chunk), to);
-        else
-            to_lds<16>(k + static_cast<int>(chunk) < bytes ? tile + (row_at[i] + chunk) : zeros, to);
-    };
-    // Load i of a period's scales.
-    auto issue_scales = [&](int p, int i) {
-        const int k = p * kRowWords;
-        const uint8_t* tile = (i < kLoadsV ? w_scale_tile : a_scale_tile) + 4 * k;
-        uint8_t* to = lds + kRing + (p & 1) * kScaleSlot + (wid + kWavesHere * i) * 256;
-        if (k + kRowWords <= words)
-            to_lds<4>(tile + (row_at[i] / 16 + 4 * word), to);
-        else
-            to_lds<4>(k + static_cast<int>(word) < words ? tile + (row_at[i] / 16 + 4 * word) : zeros, to);
-    };
-    constexpr int kIssues = kLoads + kScaleLoads;
-    f32x16 acc[MV][MN];
-#pragma unroll
-    for (int i = 0; i < MV; ++i)
-#pragma unroll
-        for (int j = 0; j < MN; ++j)
-            acc[i][j] = f32x16{};
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        issue_scales(0, i);
-        issue(0, i);
-    }
     const int wv = wid % WV * (TV / WV), wn = wid / WV * (TN / WN);
     const int frag_row = lane & 31, half = lane >> 5;
-    const int swz = swizzle(frag_row);  // rows of a tile start at multiples of 32
+
+    // Workgroups go round the eight XCDs: each XCD takes a contiguous run of tiles,
+    // rows fastest, so that the tiles that share weights share an L2; its workgroups
+    // go through the run together.
+    const int xcd = blockIdx.x & 7;
+    const int per = tiles >> 3, extra = tiles & 7;
+    const int run_end = (xcd + 1) * per + (xcd + 1 < extra ? xcd + 1 : extra);
+    const int stride = (static_cast<int>(gridDim.x) - xcd + 7) >> 3;
+    int tile = xcd * per + (xcd < extra ? xcd : extra) + static_cast<int>(blockIdx.x >> 3);
+
+    // Of a tile: its first row and entry, and the last ones' numbers in it.
+    struct Tile {
+        int v0, n0, last_v, last_n;
+    };
+    auto tile_at = [&](int t) {
+        const int v0 = t / tiles_n * TV, n0 = t % tiles_n * TN;
+        return Tile{v0, n0, cols - 1 - v0, rows - 1 - n0};
+    };
+    // Load i of a wavefront covers rows 8 (wavefront + kWavesHere * i) and on; a row's
+    // 16-byte chunks and its words of scales lie at positions XORed with the row's number,
+    // so that what the lanes read together lies in different banks.
+    const int first_row = wid * 8 + lane / 8;
+    const uint32_t chunk = (lane % 8 ^ first_row / 2 % 8) * 16;
+    const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero_chunk);
+    asm volatile("" : "+s"(zeros));  // looked up once, not in every stage
+    auto row_of = [&](const Tile& t, int i) {
+        const int row = first_row + 8 * kWavesHere * i;
+        return static_cast<uint32_t>(i < kLoadsV ? min(row, t.last_v) : min(row - TV, t.last_n));
+    };
+    // Load i of stage s of tile t, into slot `slot`.
+    auto issue = [&](const Tile& t, int s, int i, int slot) {
+        const int k = s * BK;
+        const uint8_t* from = (i < kLoadsV ? w + static_cast<size_t>(t.v0) * bytes : a + static_cast<size_t>(t.n0) * bytes) + k;
+        const uint32_t at = __umul24(row_of(t, i), bytes) + chunk;
+        uint8_t* to = lds + slot * kSlot + (wid + kWavesHere * i) * 1024;
+        if (k + BK <= bytes)
+            to_lds<16>(from + at, to);
+        else
+            to_lds<16>(k + static_cast<int>(chunk) < bytes ? from + at : zeros, to);
+    };
+    // Load i of the scales of period p of tile t.
+    auto issue_scales = [&](const Tile& t, int p, int i, int slot) {
+        const int k = p * kRowWords;
+        const uint8_t* from = (i < kLoadsV ? w_scale + static_cast<size_t>(t.v0) * words * 4
+                                           : a_scale + static_cast<size_t>(t.n0) * words * 4) + 4 * k;
+        const uint32_t word = lane % 8 ^ (wid + kWavesHere * i) % 4 * 2;
+        const uint32_t at = __umul24(row_of(t, i), words * 4) + 4 * word;
+        uint8_t* to = lds + 2 * kSlot + slot * kScaleSlot + (wid + kWavesHere * i) * 256;
+        if (k + kRowWords <= words)
+            to_lds<4>(from + at, to);
+        else
+            to_lds<4>(k + static_cast<int>(word) < words ? from + at : zeros, to);
+    };
+    f32x16 acc[MV][MN];
     // A step (a block of either half) is multiplied while the next one's fragments
     // are read: of stage s - 1 the last step waits in registers over the barrier,
     // with its scales. Reads and loads go between the matrix instructions, in whose
     // shadow they issue.
     constexpr int kReads = MV + MN, kMul = MV * MN;
-    constexpr int kHalfWords = kWords / 2;
     i32x4 fw[2][MV], fa[2][MN];
-    int sw[2][kHalfWords][MV], sa[2][kHalfWords][MN];  // of this stage, and of the one before
-    auto read = [&](int s, int step, int i) {
-        const uint8_t* slot = lds + (s & 1) * kSlot;
-        const int pos = ((half * kSteps + step) ^ swz) * 16;
+    int sw[2][MV], sa[2][MN];  // scales of this stage, and of the one before
+    const int swz = frag_row / 2 % 8;  // rows of a tile start at multiples of 32
+    auto read = [&](int slot, int step, int i) {
+        const uint8_t* at = lds + slot * kSlot + ((half * kSteps + step) ^ swz) * 16 + frag_row * BK;
         if (i < MN)
-            fa[step & 1][i] = *reinterpret_cast<const i32x4*>(slot + (TV + wn + 32 * i + frag_row) * BK + pos);
+            fa[step & 1][i] = *reinterpret_cast<const i32x4*>(at + (TV + wn + 32 * i) * BK);
         else
-            fw[step & 1][i - MN] =
-                *reinterpret_cast<const i32x4*>(slot + (wv + 32 * (i - MN) + frag_row) * BK + pos);
+            fw[step & 1][i - MN] = *reinterpret_cast<const i32x4*>(at + (wv + 32 * (i - MN)) * BK);
     };
-    auto read_scales = [&](int s, int i) {
-        const int* scales = reinterpret_cast<const int*>(lds + kRing + (s / kPeriod & 1) * kScaleSlot);
-        const int row = i < MN ? TV + wn + 32 * i + frag_row : wv + 32 * (i - MN) + frag_row;
-#pragma unroll
-        for (int h = 0; h < kHalfWords; ++h) {
-            const int v = scales[row * kRowWords + s % kPeriod * kWords + half * kHalfWords + h];
-            if (i < MN)
-                sa[0][h][i] = v;
-            else
-                sw[0][h][i - MN] = v;
-        }
+    auto read_scales = [&](int slot, int j, int i) {
+        const uint8_t* at = lds + 2 * kSlot + slot * kScaleSlot + ((2 * j + half) ^ frag_row / 8 * 2) * 4 +
+                            frag_row * (4 * kRowWords);
+        if (i < MN)
+            sa[0][i] = *reinterpret_cast<const int*>(at + (TV + wn + 32 * i) * (4 * kRowWords));
+        else
+            sw[0][i - MN] = *reinterpret_cast<const int*>(at + (wv + 32 * (i - MN)) * (4 * kRowWords));
     };
     // The last step of stage s - 1 takes the older scales.
     auto multiply = [&](int step, int m, int old) {
-        const int i = m / MN, j = m % MN, h = step / 4;
+        const int i = m / MN, j = m % MN;
         const i32x4 &x = fw[step & 1][i], &y = fa[step & 1][j];
-        const int p = sw[old][h][i], q = sa[old][h][j];
-        switch (step & 3) {
+        const int p = sw[old][i], q = sa[old][j];
+        switch (step) {
             case 0: acc[i][j] = multiply_blocks<0>(x, y, acc[i][j], p, q); break;
             case 1: acc[i][j] = multiply_blocks<1>(x, y, acc[i][j], p, q); break;
             case 2: acc[i][j] = multiply_blocks<2>(x, y, acc[i][j], p, q); break;
@@ -371,124 +360,159 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     };
     // Of `work` pieces spread over `steps` steps, the first of step n.
     auto share = [](int n, int steps, int work) { return (n * work + steps - 1) / steps; };
-#pragma unroll 1
-    for (int s0 = 0; s0 < stages; s0 += kPeriod)
-#pragma unroll
-    for (int j = 0; j < kPeriod; ++j) {
-        const int s = s0 + j;
-        if (s >= stages)
-            break;
-        // Stage s has landed; past the barrier every wavefront has also read all of
-        // stage s - 1.
-        stage_barrier<0>();
-#pragma unroll
-        for (int h = 0; h < kHalfWords; ++h) {
-#pragma unroll
-            for (int i = 0; i < MV; ++i)
-                sw[1][h][i] = sw[0][h][i];
-#pragma unroll
-            for (int j = 0; j < MN; ++j)
-                sa[1][h][j] = sa[0][h][j];
-        }
-#pragma unroll
-        for (int h = 0; h < kSteps; ++h) {
-            const int pieces = h == 0 ? 2 * kReads + kIssues : kReads;
-#pragma unroll
-            for (int m = 0; m < kMul; ++m) {
-                if (h > 0)
-                    multiply(h - 1, m, 0);
-                else if (s > 0)
-                    multiply(kSteps - 1, m, 1);
-#pragma unroll
-                for (int p = share(m, kMul, pieces); p < share(m + 1, kMul, pieces); ++p) {
-                    if (p < kReads)
-                        read(s, h, p);
-                    else if (p < 2 * kReads)
-                        read_scales(s, p - kReads);
-                    else if (p < 2 * kReads + kLoads)
-                        issue(s + 1, p - 2 * kReads);
-                    else
-                        issue_scales(s / kPeriod + 1, p - 2 * kReads - kLoads + kScaleLoads * j);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < kMul; ++m)
-        multiply(kSteps - 1, m, 0);
-    // No load may still be on its way into LDS when it is used again.
-    stage_barrier<0>();
+    constexpr int kPieces = 2 * kReads + kLoads + kScaleLoads;
 
-    // Lane l holds entries 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32 of a
-    // 32 x 32 tile. Turned through LDS (each wavefront in its own part), they go
-    // out as 16-byte stores along the rows.
-    uint8_t* turn = lds + wid * kTurn;
-    const bool whole = (static_cast<size_t>(cols) * ESZ) % 16 == 0 &&
-                       (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    Tile cur = tile_at(tile);
 #pragma unroll
-    for (int j = 0; j < MN; ++j) {
-        const int nb = n0 + wn + 32 * j;
+    for (int i = 0; i < kLoads; ++i) {
+        issue_scales(cur, 0, i, 0);
+        issue(cur, 0, i, 0);
+    }
+    stage_barrier<0>();
+    int slot = 0, scale_slot = 0;  // of the stage and the period at hand
+#pragma unroll 1
+    for (;;) {
+        tile += stride;
+        const bool more = tile < run_end;
+        const Tile next = more ? tile_at(tile) : cur;
 #pragma unroll
         for (int i = 0; i < MV; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int at_v = 32 * i + 8 * e + 4 * half;
-                const float z[4] = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
-                                    acc[i][j][4 * e + 3]};
-                uint8_t* to = turn + (lane & 31) * kRowBytes + at_v * ESZ;
-                if constexpr (OUT == kBF16)
-                    *reinterpret_cast<uint2*>(to) = make_uint2(
-                        __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{z[0], z[1]}, bf16x2)),
-                        __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{z[2], z[3]}, bf16x2)));
-                else
-                    *reinterpret_cast<float4*>(to) = make_float4(z[0], z[1], z[2], z[3]);
-            }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        constexpr int kEntries = 32 * MV;
-        if (whole) {
-            constexpr int kPer = 16 / ESZ;               // entries per store
-            constexpr int kLanes = kEntries / kPer;      // lanes per row
+            for (int j = 0; j < MN; ++j)
+                acc[i][j] = f32x16{};
+#pragma unroll 1
+        for (int s0 = 0; s0 < stages; s0 += kPeriod) {
 #pragma unroll
-            for (int t = 0; t < 32 * kLanes / 64; ++t) {
-                const int r = t * (64 / kLanes) + lane / kLanes, c = lane % kLanes * kPer;
-                const uint4 x = *reinterpret_cast<const uint4*>(turn + r * kRowBytes + c * ESZ);
-                const int v = v0 + wv + c;
-                if (nb + r < rows && v < cols)
-                    *reinterpret_cast<uint4*>(static_cast<char*>(out) +
-                                              (static_cast<size_t>(nb + r) * cols + v) * ESZ) = x;
-            }
-        } else {
-            using elem_t = typename std::conditional<OUT == kBF16, uint16_t, uint32_t>::type;
-            for (int r = 0; r < 32 && nb + r < rows; ++r)
+            for (int j = 0; j < kPeriod; ++j) {
+                const int s = s0 + j;
+                if (s >= stages)
+                    break;
+                // Stage s has landed; past the barrier every wavefront has also read all of
+                // stage s - 1. (The first one's is the barrier before.)
+                if (s > 0) {
+                    stage_barrier<0>();
+                    slot ^= 1;
+                }
+                const bool last = s + 1 == stages;
 #pragma unroll
-                for (int c = lane; c < kEntries; c += 64)
-                    if (v0 + wv + c < cols)
-                        static_cast<elem_t*>(out)[static_cast<size_t>(nb + r) * cols + v0 + wv + c] =
-                            *reinterpret_cast<const elem_t*>(turn + r * kRowBytes + c * ESZ);
+                for (int i = 0; i < MV; ++i)
+                    sw[1][i] = sw[0][i];
+#pragma unroll
+                for (int i = 0; i < MN; ++i)
+                    sa[1][i] = sa[0][i];
+#pragma unroll
+                for (int h = 0; h < kSteps; ++h) {
+                    const int pieces = h == 0 ? kPieces : kReads;
+#pragma unroll
+                    for (int m = 0; m < kMul; ++m) {
+                        if (h > 0)
+                            multiply(h - 1, m, 0);
+                        else if (s > 0)
+                            multiply(kSteps - 1, m, 1);
+#pragma unroll
+                        for (int p = share(m, kMul, pieces); p < share(m + 1, kMul, pieces); ++p) {
+                            if (p < kReads)
+                                read(slot, h, p);
+                            else if (p < 2 * kReads)
+                                read_scales(scale_slot, j, p - kReads);
+                            else if (p < 2 * kReads + kLoads)
+                                issue(last ? next : cur, last ? 0 : s + 1, p - 2 * kReads, slot ^ 1);
+                            else  // of the period behind, or the next tile's first
+                                issue_scales(s0 + kPeriod < stages ? cur : next, s0 + kPeriod < stages ? s0 / kPeriod + 1 : 0,
+                                             p - 2 * kReads - kLoads + kScaleLoads * j, scale_slot ^ 1);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                if (last && j < kPeriod - 1) {  // the shares of stages that this tile does not have
+#pragma unroll
+                    for (int i = kScaleLoads * (j + 1); i < kLoads; ++i)
+                        issue_scales(next, 0, i, scale_slot ^ 1);
+                }
+            }
+            scale_slot ^= 1;
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int m = 0; m < kMul; ++m)
+            multiply(kSteps - 1, m, 0);
+        // The next tile's first stage has landed, and the last stage's slot is free.
+        stage_barrier<0>();
+
+        // Lane l holds entries 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32 of a
+        // 32 x 32 tile. Turned through LDS (each wavefront in its own part), they go
+        // out as 16-byte stores along the rows, which nobody waits for before the next
+        // tile's second stage.
+        uint8_t* turn = lds + slot * kSlot + wid * kTurn;
+        const bool whole = (static_cast<size_t>(cols) * ESZ) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+#pragma unroll
+        for (int j = 0; j < MN; ++j) {
+            const int nb = cur.n0 + wn + 32 * j;
+#pragma unroll
+            for (int i0 = 0; i0 < MV; i0 += kTurnV) {
+#pragma unroll
+                for (int i = 0; i < kTurnV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x16& f = acc[i0 + i][j];
+                        const float z[4] = {f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]};
+                        uint8_t* to = turn + frag_row * kRowBytes + (32 * i + 8 * e + 4 * half) * ESZ;
+                        if constexpr (OUT == kBF16)
+                            *reinterpret_cast<uint2*>(to) = make_uint2(
+                                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{z[0], z[1]}, bf16x2)),
+                                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{z[2], z[3]}, bf16x2)));
+                        else
+                            *reinterpret_cast<float4*>(to) = make_float4(z[0], z[1], z[2], z[3]);
+                    }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                constexpr int kEntries = 32 * kTurnV;
+                const int vb = cur.v0 + wv + 32 * i0;
+                if (whole) {
+                    constexpr int kPer = 16 / ESZ;  // entries per store, eight lanes per row
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int r = t * 8 + lane / 8, c = lane % 8 * kPer;
+                        const uint4 x = *reinterpret_cast<const uint4*>(turn + r * kRowBytes + c * ESZ);
+                        if (nb + r < rows && vb + c < cols)
+                            *reinterpret_cast<uint4*>(static_cast<char*>(out) +
+                                                      (static_cast<size_t>(nb + r) * cols + vb + c) * ESZ) = x;
+                    }
+                } else {
+                    using elem_t = typename std::conditional<OUT == kBF16, uint16_t, uint32_t>::type;
+                    for (int r = 0; r < 32 && nb + r < rows; ++r)
+                        if (lane < kEntries && vb + lane < cols)
+                            static_cast<elem_t*>(out)[static_cast<size_t>(nb + r) * cols + vb + lane] =
+                                *reinterpret_cast<const elem_t*>(turn + r * kRowBytes + lane * ESZ);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            }
+        }
+        if (!more)
+            return;
+        cur = next;
+        slot ^= 1;
+        lds_barrier();  // all outputs have left LDS
     }
 }
 
-template <int TV, int TN, int WV, int WN, int BK>
+template <int TV, int TN, int WV, int WN, int PER_CU>
 hipError_t launch_tile(int rows, int depth, int cols, const uint8_t* a, const uint8_t* a_scale,
                        const uint8_t* w, const uint8_t* w_scale, int out_dtype, void* out, hipStream_t s) {
     const long tiles_v = (static_cast<long>(cols) + TV - 1) / TV;
     const long tiles_n = (static_cast<long>(rows) + TN - 1) / TN;
-    if (tiles_v * tiles_n >= (1L << 32) / (64 * WV * WN))
+    if (tiles_v * tiles_n >= 1L << 31)
         return hipErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(tiles_v * tiles_n)), block(64 * WV * WN);
+    // Workgroups stay for several tiles: as many as the chip holds at a time.
+    const dim3 grid(static_cast<unsigned>(std::min(tiles_v * tiles_n, 256L * PER_CU))), block(64 * WV * WN);
     if (out_dtype == SPEC_BF16)
-        mxfp4_product_kernel<TV, TN, WV, WN, BK, kBF16><<<grid, block, 0, s>>>(
+        mxfp4_product_kernel<TV, TN, WV, WN, kBF16><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     else
-        mxfp4_product_kernel<TV, TN, WV, WN, BK, kF32><<<grid, block, 0, s>>>(
+        mxfp4_product_kernel<TV, TN, WV, WN, kF32><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     return hipGetLastError();
@@ -559,11 +583,11 @@ int spec_mxfp4_product(int rows, int depth, int cols, const uint8_t* a, const ui
 #define SPEC_TILE(...) \
     e = launch_tile<__VA_ARGS__>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s)
     if (rows > 128 && tiles(256, 256) >= 224)
-        SPEC_TILE(256, 256, 2, 4, 128);
+        SPEC_TILE(256, 256, 2, 4, 1);
     else if (rows > 64 && tiles(128, 128) >= 448)
-        SPEC_TILE(128, 128, 2, 2, 128);
+        SPEC_TILE(128, 128, 2, 2, 2);
     else
-        SPEC_TILE(64, 64, 2, 1, 128);
+        SPEC_TILE(64, 64, 1, 2, 4);
 #undef SPEC_TILE
     return e == hipSuccess ? SPEC_OK : e == hipErrorInvalidValue ? SPEC_EINVAL : SPEC_EHIP;
 }
