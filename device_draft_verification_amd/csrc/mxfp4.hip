@@ -298,29 +298,20 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
         const int row = first_row + 8 * kWavesHere * i;
         return static_cast<uint32_t>(i < kLoadsV ? min(row, t.last_v) : min(row - TV, t.last_n));
     };
-    // Load i of stage s of tile t, into slot `slot`.
+    // Load i of stage s of tile t, into slot `slot`. Chunks past the depth are the row's
+    // last one again: their scales are 2^-127 on either side, and make them nothing.
     auto issue = [&](const Tile& t, int s, int i, int slot) {
-        const int k = s * BK;
-        const uint8_t* from = (i < kLoadsV ? w + static_cast<size_t>(t.v0) * bytes : a + static_cast<size_t>(t.n0) * bytes) + k;
-        const uint32_t at = __umul24(row_of(t, i), bytes) + chunk;
-        uint8_t* to = lds + slot * kSlot + (wid + kWavesHere * i) * 1024;
-        if (k + BK <= bytes)
-            to_lds<16>(from + at, to);
-        else
-            to_lds<16>(k + static_cast<int>(chunk) < bytes ? from + at : zeros, to);
+        const uint8_t* from = i < kLoadsV ? w + static_cast<size_t>(t.v0) * bytes : a + static_cast<size_t>(t.n0) * bytes;
+        const uint32_t at = __umul24(row_of(t, i), bytes) + min(s * BK + static_cast<int>(chunk), bytes - 16);
+        to_lds<16>(from + at, lds + slot * kSlot + (wid + kWavesHere * i) * 1024);
     };
-    // Load i of the scales of period p of tile t.
+    // Load i of the scales of period p of tile t, zeros past the depth.
     auto issue_scales = [&](const Tile& t, int p, int i, int slot) {
-        const int k = p * kRowWords;
-        const uint8_t* from = (i < kLoadsV ? w_scale + static_cast<size_t>(t.v0) * words * 4
-                                           : a_scale + static_cast<size_t>(t.n0) * words * 4) + 4 * k;
-        const uint32_t word = lane % 8 ^ (wid + kWavesHere * i) % 4 * 2;
+        const uint8_t* from = i < kLoadsV ? w_scale + static_cast<size_t>(t.v0) * words * 4
+                                          : a_scale + static_cast<size_t>(t.n0) * words * 4;
+        const int word = p * kRowWords + static_cast<int>(lane % 8 ^ (wid + kWavesHere * i) % 4 * 2);
         const uint32_t at = __umul24(row_of(t, i), words * 4) + 4 * word;
-        uint8_t* to = lds + 2 * kSlot + slot * kScaleSlot + (wid + kWavesHere * i) * 256;
-        if (k + kRowWords <= words)
-            to_lds<4>(from + at, to);
-        else
-            to_lds<4>(k + static_cast<int>(word) < words ? from + at : zeros, to);
+        to_lds<4>(word < words ? from + at : zeros, lds + 2 * kSlot + slot * kScaleSlot + (wid + kWavesHere * i) * 256);
     };
     f32x16 acc[MV][MN];
     // A step (a block of either half) is multiplied while the next one's fragments
@@ -382,7 +373,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                 acc[i][j] = f32x16{};
 #pragma unroll 1
         for (int s0 = 0; s0 < stages; s0 += kPeriod) {
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < kPeriod; ++j) {
                 const int s = s0 + j;
                 if (s >= stages)
@@ -425,7 +416,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                     }
                 }
                 if (last && j < kPeriod - 1) {  // the shares of stages that this tile does not have
-#pragma unroll
+#pragma unroll 1
                     for (int i = kScaleLoads * (j + 1); i < kLoads; ++i)
                         issue_scales(next, 0, i, scale_slot ^ 1);
                 }
