@@ -146,6 +146,11 @@ struct Eight {
     }
 };
 
+// The exponent comes from the largest magnitude's bits; the conversion instructions
+// scale, round to nearest even and saturate. Bound by memory: 152064 x 4096 bf16 with
+// their values in place take 454 us, 6.2 TB/s, the rate of a large copy; 2304 x 4001
+// fp32, whose rows start anywhere, 13.5 us.
+//
 // A lane takes eight entries, four lanes a block, 16 blocks a wavefront, over all
 // rows as one sequence (a padded row is a whole number of lanes' entries, 16 or
 // more), so that codes go out as one stream.
@@ -196,23 +201,36 @@ __global__ __launch_bounds__(kBlock) void mxfp4_quantize_kernel(const void* x, i
 
 // ----------------------------------------------------------------- product ---
 
-// A workgroup of WV x WN wavefronts forms a TV (vocabulary) x TN (rows) tile of
+// A workgroup of WV x WN wavefronts forms TV (vocabulary) x TN (rows) tiles of
 // the output, each wavefront TV / WV x TN / WN as 32 x 32 tiles of
 // v_mfma_scale_f32_32x32x64_f8f6f4, in which a lane holds one block of 32 codes
 // (16 bytes) of its row and that block's scale. The vocabulary is the M side: a
 // lane then holds runs of four consecutive outputs of one row.
 //
-// K in stages of BK bytes of codes through a ring of LDS slots, loaded straight
-// into LDS RING - 1 stages ahead: one barrier per stage, after which the slot of
-// the stage before is refilled. A slot holds TV + TN rows of BK bytes; a row's
-// 16-byte chunks sit at positions XORed with the row's number in units of the
-// banks' 256 bytes, so that the rows that a phase of a fragment read touches lie
-// in different places. Behind them lie the rows' scales, BK / 16 bytes each.
-// Which block of K an instruction multiplies is free as long as both sides agree:
-// in a stage the lower half of the lanes takes the first half of the blocks, the
-// upper half the second, so that a lane's scales of a stage are whole words.
-// Rows past the end repeat the last one (their outputs are not stored), chunks
-// and scales past the depth come from a page of zeros.
+// K in stages of BK bytes of codes through two LDS slots, loaded straight into
+// LDS: one barrier per stage, after which the slot of the stage before is filled
+// with the one behind. A slot holds TV + TN rows of BK bytes; a row's 16-byte
+// chunks sit at positions XORed with the row's number, so that the rows that a
+// phase of a fragment read touches lie in different banks. Scales come for four
+// stages at a time: a row's 8 bytes of a stage would cost as many requests as its
+// 128 bytes of codes. Which block of K an instruction multiplies is free as long
+// as both sides agree: in a stage the lower half of the lanes takes the first half
+// of the blocks, the upper half the second, so that a lane's scales of a stage are
+// a word. Rows past the end repeat the last one (their outputs are not stored),
+// scales past the depth come from a page of zeros.
+//
+// Workgroups stay for several tiles; the first loads of the next one run through
+// the epilogue, which turns the outputs in LDS so that stores are whole lines.
+//
+// Many rows are bound by the matrix instructions and by LDS, which carries 192 KB
+// of reads and 68 KB of writes a stage of 256 x 256: 2304 x 152064 outputs at depth
+// 4096 take 777 us, 3.7 PFLOP/s, where a loop of nothing but these instructions
+// reaches 6.2 to 6.8 on such data (the clock falls under their power) and the
+// kernel without its loads took 557. Few rows are bound by the read of the weights
+// and its latency: 64 x 152064 at depth 4096 take 83 us, 4.2 TB/s, 1 x 152064 62 us,
+// 5.3 TB/s, 1 x 32000 14.7 us, 4.7 TB/s. Slower: stages of half the length and four
+// slots 860 us for 777, 4 wavefronts of 128 x 128 each (registers spill). Weights
+// straight into registers, the rows whole in LDS: 85 us for 83.
 __device__ int4 zero_chunk;  // zero from load on, never written
 
 // SIZE bytes a lane from memory into LDS, behind one another there.
@@ -246,18 +264,18 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     constexpr int kLoadsV = TV / 8 / kWavesHere;      // of them of the vocabulary
     constexpr int kPeriod = 4;                        // stages whose scales are loaded together: a word
     constexpr int kRowWords = 2 * kPeriod;            // of scales for 64 bytes of codes
-    constexpr int kScaleLoads = kLoads / kPeriod;     // per wavefront and stage
+    constexpr int kScaleLoads = (kLoads + kPeriod - 1) / kPeriod;  // per wavefront and stage, at most
     constexpr int kSlot = kRows * BK;
     constexpr int kScaleSlot = kRows * 4 * kRowWords;
     constexpr int kSteps = BK / 32;                   // of two blocks each
-    static_assert(TV % (8 * kWavesHere) == 0 && TN % (8 * kWavesHere) == 0 && kLoads % kPeriod == 0,
+    static_assert(TV % (8 * kWavesHere) == 0 && TN % (8 * kWavesHere) == 0,
                   "every wavefront issues the same loads");
     static_assert(kWavesHere % 2 == 0, "a lane's chunk is the same in all loads");
-    // The epilogue turns 32 rows x 128 bytes of a wavefront's outputs through LDS at a
-    // time, in the slot of the last stage.
+    // The epilogue turns 32 rows of up to 128 bytes of a wavefront's outputs through LDS
+    // at a time, in the slot of the last stage.
     constexpr int ESZ = OUT == kBF16 ? 2 : 4;
-    constexpr int kTurnV = 128 / ESZ / 32;            // fragments of the vocabulary at a time
-    constexpr int kRowBytes = 128 + 16;
+    constexpr int kTurnV = MV == 1 ? 1 : 128 / ESZ / 32;  // fragments of the vocabulary at a time
+    constexpr int kTurnBytes = 32 * kTurnV * ESZ, kRowBytes = kTurnBytes + 16;
     constexpr int kTurn = 32 * kRowBytes;
     static_assert(MV % kTurnV == 0 && kWavesHere * kTurn <= kSlot, "outputs turn inside a slot");
     // One LDS object: with two the compiler keeps their accesses apart by alias
@@ -408,9 +426,11 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                                 read_scales(scale_slot, j, p - kReads);
                             else if (p < 2 * kReads + kLoads)
                                 issue(last ? next : cur, last ? 0 : s + 1, p - 2 * kReads, slot ^ 1);
-                            else  // of the period behind, or the next tile's first
+                            else if (const int i = p - 2 * kReads - kLoads + kScaleLoads * j;
+                                     kLoads % kPeriod == 0 || i < kLoads)
+                                // of the period behind, or the next tile's first
                                 issue_scales(s0 + kPeriod < stages ? cur : next, s0 + kPeriod < stages ? s0 / kPeriod + 1 : 0,
-                                             p - 2 * kReads - kLoads + kScaleLoads * j, scale_slot ^ 1);
+                                             i, scale_slot ^ 1);
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
@@ -460,10 +480,10 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                 constexpr int kEntries = 32 * kTurnV;
                 const int vb = cur.v0 + wv + 32 * i0;
                 if (whole) {
-                    constexpr int kPer = 16 / ESZ;  // entries per store, eight lanes per row
+                    constexpr int kPer = 16 / ESZ, kLanes = kTurnBytes / 16;  // entries per store, lanes per row
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int r = t * 8 + lane / 8, c = lane % 8 * kPer;
+                    for (int t = 0; t < kLanes / 2; ++t) {
+                        const int r = t * (64 / kLanes) + lane / kLanes, c = lane % kLanes * kPer;
                         const uint4 x = *reinterpret_cast<const uint4*>(turn + r * kRowBytes + c * ESZ);
                         if (nb + r < rows && vb + c < cols)
                             *reinterpret_cast<uint4*>(static_cast<char*>(out) +
@@ -494,7 +514,7 @@ hipError_t launch_tile(int rows, int depth, int cols, const uint8_t* a, const ui
                        const uint8_t* w, const uint8_t* w_scale, int out_dtype, void* out, hipStream_t s) {
     const long tiles_v = (static_cast<long>(cols) + TV - 1) / TV;
     const long tiles_n = (static_cast<long>(rows) + TN - 1) / TN;
-    if (tiles_v * tiles_n >= 1L << 31)
+    if (tiles_v * tiles_n > (1L << 31) - 4096)  // a workgroup counts on to its next tile
         return hipErrorInvalidValue;
     // Workgroups stay for several tiles: as many as the chip holds at a time.
     const dim3 grid(static_cast<unsigned>(std::min(tiles_v * tiles_n, 256L * PER_CU))), block(64 * WV * WN);
@@ -573,12 +593,22 @@ int spec_mxfp4_product(int rows, int depth, int cols, const uint8_t* a, const ui
     hipError_t e;
 #define SPEC_TILE(...) \
     e = launch_tile<__VA_ARGS__>(rows, depth, cols, a, a_scale, w, w_scale, out_dtype, out, s)
-    if (rows > 128 && tiles(256, 256) >= 224)
+    // The larger the tile, the less of the codes goes through LDS for a product, but the
+    // fewer workgroups there are and the more rows may be empty. Measured at a depth of 4096
+    // (us; the rule's side first): 256 against 128 with 196 tiles of 256 (256 rows, 50000
+    // entries) 44 : 56, with 158 (512, 20000) 37 : 44; 128 against 256 with 125 (192, 32000)
+    // 30 : 36. 128 against 64 with 250 tiles of 128 (128, 32000) 25 : 28; 64 against 128 with
+    // 157 (100, 20011, depth 1024) 7.8 : 9.4, and with 64 rows and 152064 entries 83 : 82.
+    // 64 against 32 with 33 rows and 32000 entries 21.5 : 23.0, with 64 and 152064 83 : 93;
+    // 32 against 64 with 32 rows 20.8 : 21.6, and with 152064 entries 69.8 : 74.7.
+    if (rows > 128 && tiles(256, 256) >= 144)
         SPEC_TILE(256, 256, 2, 4, 1);
-    else if (rows > 64 && tiles(128, 128) >= 448)
+    else if (rows > 64 && tiles(128, 128) >= 224)
         SPEC_TILE(128, 128, 2, 2, 2);
-    else
+    else if (rows > 32)
         SPEC_TILE(64, 64, 1, 2, 4);
+    else
+        SPEC_TILE(64, 32, 2, 1, 5);
 #undef SPEC_TILE
     return e == hipSuccess ? SPEC_OK : e == hipErrorInvalidValue ? SPEC_EINVAL : SPEC_EHIP;
 }

@@ -42,8 +42,8 @@
  * quantisation; x, out_values and out are aligned to their element. Any D >= 1
  * and V >= 1, N >= 0; depth is D'. out_values may be x itself (the values then
  * take its place); no other overlap. Each call is one dispatch: N * D' < 2^35
- * in the quantisation, and the tiles of the output in the product (N < 2^31 -
- * 256 for the narrowest); SPEC_EINVAL beyond.
+ * in the quantisation, and in the product at most 2^31 - 4096 tiles of up to 256
+ * rows x 256 entries; SPEC_EINVAL beyond.
  *
  * Asynchrony and errors: as in spec_verify.h; each call enqueues one kernel on
  * hip_stream (a hipStream_t, NULL = the null stream), needs no workspace, and

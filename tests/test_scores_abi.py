@@ -132,8 +132,11 @@ def test_products_and_quantisations_of_many_rows(shim):  # noqa: F811
               ((1, 1), (1, (1 << 31) - 200), (1 << 23, 2047), ((1 << 28) - 16, 1)) for t in (0, 1) for v in (None, "p3")]
     for c, (rc, n, items) in zip(calls, run(shim, calls)):
         assert rc == 0 and n == 1 and 0 < items < 1 << 32, (c, rc, n, items)
-    for c, (rc, n, _) in zip(calls, run(shim, [call(1 << 20, 128, 1 << 20, t) for t in (0, 1)])):
-        assert rc == E and n == 0
+    # 2^23 tiles of rows: with 255 of the vocabulary a dispatch, with 256 too many
+    for v, want in ((1 << 20, (OK, 1)), (255 * 256, (OK, 1)), (255 * 256 + 1, (E, 0))):
+        n = 1 << 20 if v == 1 << 20 else (1 << 31) - 1
+        for rc, launched, _ in run(shim, [call(n, 128, v, t) for t in (0, 1)]):
+            assert (rc, launched) == want, (n, v)
 
 
 def test_a_context_takes_streams_of_its_own_device_only(two_devices):  # noqa: F811
