@@ -30,7 +30,7 @@
  * positive and finite or has a reciprocal that overflows, has NaN in every
  * float output, rank -1 and tokens -1.
  * Arithmetic: exponentials in binary32, sums in binary64 over binary32 sums of
- * one 16-byte load, logarithms in binary64; each output rounded once to
+ * up to four 16-byte loads, logarithms in binary64; each output rounded once to
  * binary32. log S is within 2^-23 (ln V + 6) of the exact value before that.
  *
  * Backward, with a = grad_logprob[n], b = grad_entropy[n] (NULL: 0):
