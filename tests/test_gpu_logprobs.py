@@ -114,7 +114,8 @@ def test_scores(N, V, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("N,V,K", [(1024, 2500, 64), (1500, 9000, 8), (1030, 33000, 20), (600, 20000, 3)])
+@pytest.mark.parametrize("N,V,K", [(1024, 2500, 64), (1500, 9000, 8), (1030, 33000, 20), (600, 20000, 3),
+                                   (640, 20011, 64), (641, 20011, 64), (256, 60000, 33)])
 def test_scores_of_many_rows(N, V, K, dtype):
     print(f"\n[scores N={N} V={V} K={K} {dtype}]", flush=True)
     z, token, temperature = rows(N, V, N + V + K)

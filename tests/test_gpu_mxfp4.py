@@ -154,6 +154,10 @@ def test_product(N, D, V, dtype):
 @pytest.mark.parametrize("N,D,V", [
     (33, 128, 51203), (64, 384, 51200), (65, 128, 57347), (128, 640, 57344), (129, 128, 28673), (300, 256, 28675),
     (257, 1152, 28672), (512, 2176, 14336),
+    # several tiles for a workgroup of every tile, of one stage, two, three and five
+    (3, 128, 90001), (20, 384, 85000), (32, 640, 82000), (5, 1152, 82003), (40, 128, 70001), (64, 384, 66000),
+    (33, 640, 65700), (60, 1152, 65601), (70, 128, 70001), (128, 384, 66003), (100, 640, 66000), (66, 1152, 65700),
+    (512, 128, 33000), (300, 384, 36001), (257, 640, 33003), (512, 1152, 32900),
 ])
 def test_product_in_the_larger_tiles(N, D, V, dtype):
     print(f"\n[mxfp4 N={N} D={D} V={V} {dtype}]", flush=True)
