@@ -207,30 +207,30 @@ __global__ __launch_bounds__(kBlock) void mxfp4_quantize_kernel(const void* x, i
 // (16 bytes) of its row and that block's scale. The vocabulary is the M side: a
 // lane then holds runs of four consecutive outputs of one row.
 //
-// K in stages of BK bytes of codes through two LDS slots, loaded straight into
-// LDS: one barrier per stage, after which the slot of the stage before is filled
-// with the one behind. A slot holds TV + TN rows of BK bytes; a row's 16-byte
-// chunks sit at positions XORed with the row's number, so that the rows that a
-// phase of a fragment read touches lie in different banks. Scales come for four
-// stages at a time: a row's 8 bytes of a stage would cost as many requests as its
-// 128 bytes of codes. Which block of K an instruction multiplies is free as long
-// as both sides agree: in a stage the lower half of the lanes takes the first half
-// of the blocks, the upper half the second, so that a lane's scales of a stage are
-// a word. Rows past the end repeat the last one (their outputs are not stored),
-// scales past the depth come from a page of zeros.
+// K in stages of BK bytes of codes through RING LDS slots, loaded straight into
+// LDS RING - 1 stages ahead (a tile has as many at least): one barrier per stage,
+// after which the slot of the stage before is filled again. A slot holds TV + TN
+// rows of BK bytes; a row's 16-byte chunks sit at positions XORed with the row's
+// number, so that the rows that a phase of a fragment read touches lie in different
+// banks. Scales come for four stages at a time: a row's 8 bytes of a stage would
+// cost as many requests as its 128 bytes of codes. Which block of K an instruction
+// multiplies is free as long as both sides agree: in a stage the lower half of the
+// lanes takes the first half of the blocks, the upper half the second, so that a
+// lane's scales of a stage are a word. Rows past the end repeat the last one (their
+// outputs are not stored), scales past the depth come from a page of zeros.
 //
 // Workgroups stay for several tiles; the first loads of the next one run through
 // the epilogue, which turns the outputs in LDS so that stores are whole lines.
 //
 // Many rows are bound by the matrix instructions and by LDS, which carries 192 KB
 // of reads and 68 KB of writes a stage of 256 x 256: 2304 x 152064 outputs at depth
-// 4096 take 777 us, 3.7 PFLOP/s, where a loop of nothing but these instructions
+// 4096 take 780-815 us, 3.6 PFLOP/s, where a loop of nothing but these instructions
 // reaches 6.2 to 6.8 on such data (the clock falls under their power) and the
 // kernel without its loads took 557. Few rows are bound by the read of the weights
-// and its latency: 64 x 152064 at depth 4096 take 83 us, 4.2 TB/s, 1 x 152064 62 us,
-// 5.3 TB/s, 1 x 32000 14.7 us, 4.7 TB/s. Slower: stages of half the length and four
-// slots 860 us for 777, 4 wavefronts of 128 x 128 each (registers spill). Weights
-// straight into registers, the rows whole in LDS: 85 us for 83.
+// and its latency: 64 x 152064 at depth 4096 take 79 us, 4.4 TB/s, 1 x 152064 60 us,
+// 5.5 TB/s, 1 x 32000 14 us, 5 TB/s. Slower: stages of half the length and four
+// slots 860 us (then 810), 4 wavefronts of 128 x 128 each, alone on their SIMDs, 885.
+// Weights straight into registers, the rows whole in LDS: 85 us for 64 x 152064.
 __device__ int4 zero_chunk;  // zero from load on, never written
 
 // SIZE bytes a lane from memory into LDS, behind one another there.
@@ -251,8 +251,8 @@ __device__ __forceinline__ f32x16 multiply_blocks(const i32x4& a, const i32x4& b
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
-template <int TV, int TN, int WV, int WN, int OUT>
-__global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
+template <int TV, int TN, int WV, int WN, int RING, int OUT>
+__global__ __launch_bounds__(64 * WV * WN, RING > 2 ? 1 : 2) void mxfp4_product_kernel(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_scale, const uint8_t* __restrict__ w,
     const uint8_t* __restrict__ w_scale, int rows, int depth, int cols, int tiles_n, int tiles,
     void* __restrict__ out) {
@@ -264,7 +264,11 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     constexpr int kLoadsV = TV / 8 / kWavesHere;      // of them of the vocabulary
     constexpr int kPeriod = 4;                        // stages whose scales are loaded together: a word
     constexpr int kRowWords = 2 * kPeriod;            // of scales for 64 bytes of codes
-    constexpr int kScaleLoads = (kLoads + kPeriod - 1) / kPeriod;  // per wavefront and stage, at most
+    constexpr int kAhead = RING - 1;                  // stages that loads run ahead
+    // Scales' loads are out by the stage of a period from which on they may not have
+    // landed by its end: per wavefront and stage, at most.
+    constexpr int kScaleStages = kPeriod + 1 - kAhead;
+    constexpr int kScaleLoads = (kLoads + kScaleStages - 1) / kScaleStages;
     constexpr int kSlot = kRows * BK;
     constexpr int kScaleSlot = kRows * 4 * kRowWords;
     constexpr int kSteps = BK / 32;                   // of two blocks each
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
     static_assert(MV % kTurnV == 0 && kWavesHere * kTurn <= kSlot, "outputs turn inside a slot");
     // One LDS object: with two the compiler keeps their accesses apart by alias
     // scopes, and then waits for every load into LDS before any read of it.
-    __shared__ __align__(16) uint8_t lds[2 * kSlot + 2 * kScaleSlot];
+    __shared__ __align__(16) uint8_t lds[RING * kSlot + 2 * kScaleSlot];
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int bytes = depth / 2, words = depth / 128;  // of a row: codes, words of scales
@@ -329,7 +333,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                                           : a_scale + static_cast<size_t>(t.n0) * words * 4;
         const int word = p * kRowWords + static_cast<int>(lane % 8 ^ (wid + kWavesHere * i) % 4 * 2);
         const uint32_t at = __umul24(row_of(t, i), words * 4) + 4 * word;
-        to_lds<4>(word < words ? from + at : zeros, lds + 2 * kSlot + slot * kScaleSlot + (wid + kWavesHere * i) * 256);
+        to_lds<4>(word < words ? from + at : zeros, lds + RING * kSlot + slot * kScaleSlot + (wid + kWavesHere * i) * 256);
     };
     f32x16 acc[MV][MN];
     // A step (a block of either half) is multiplied while the next one's fragments
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
             fw[step & 1][i - MN] = *reinterpret_cast<const i32x4*>(at + (wv + 32 * (i - MN)) * BK);
     };
     auto read_scales = [&](int slot, int j, int i) {
-        const uint8_t* at = lds + 2 * kSlot + slot * kScaleSlot + ((2 * j + half) ^ frag_row / 8 * 2) * 4 +
+        const uint8_t* at = lds + RING * kSlot + slot * kScaleSlot + ((2 * j + half) ^ frag_row / 8 * 2) * 4 +
                             frag_row * (4 * kRowWords);
         if (i < MN)
             sa[0][i] = *reinterpret_cast<const int*>(at + (TV + wn + 32 * i) * (4 * kRowWords));
@@ -373,12 +377,17 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
 
     Tile cur = tile_at(tile);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
+    for (int i = 0; i < kLoads; ++i)
         issue_scales(cur, 0, i, 0);
-        issue(cur, 0, i, 0);
-    }
-    stage_barrier<0>();
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            issue(cur, s, i, s);
+    constexpr int kYounger = kLoads * (RING - 2);  // loads that may be out when a stage begins
+    stage_barrier<kYounger>();
     int slot = 0, scale_slot = 0;  // of the stage and the period at hand
+    auto in_ring = [](int s) { return s >= RING ? s - RING : s; };
 #pragma unroll 1
     for (;;) {
         tile += stride;
@@ -399,10 +408,11 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                 // Stage s has landed; past the barrier every wavefront has also read all of
                 // stage s - 1. (The first one's is the barrier before.)
                 if (s > 0) {
-                    stage_barrier<0>();
-                    slot ^= 1;
+                    stage_barrier<kYounger>();
+                    slot = in_ring(slot + 1);
                 }
-                const bool last = s + 1 == stages;
+                const bool last = s + 1 == stages, over = s + kAhead >= stages;
+                const int ahead = over ? s + kAhead - stages : s + kAhead, ahead_slot = in_ring(slot + kAhead);
 #pragma unroll
                 for (int i = 0; i < MV; ++i)
                     sw[1][i] = sw[0][i];
@@ -425,9 +435,9 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                             else if (p < 2 * kReads)
                                 read_scales(scale_slot, j, p - kReads);
                             else if (p < 2 * kReads + kLoads)
-                                issue(last ? next : cur, last ? 0 : s + 1, p - 2 * kReads, slot ^ 1);
+                                issue(over ? next : cur, ahead, p - 2 * kReads, ahead_slot);
                             else if (const int i = p - 2 * kReads - kLoads + kScaleLoads * j;
-                                     kLoads % kPeriod == 0 || i < kLoads)
+                                     kLoads == kScaleLoads * kPeriod || i < kLoads)
                                 // of the period behind, or the next tile's first
                                 issue_scales(s0 + kPeriod < stages ? cur : next, s0 + kPeriod < stages ? s0 / kPeriod + 1 : 0,
                                              i, scale_slot ^ 1);
@@ -446,8 +456,11 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
 #pragma unroll
         for (int m = 0; m < kMul; ++m)
             multiply(kSteps - 1, m, 0);
-        // The next tile's first stage has landed, and the last stage's slot is free.
-        stage_barrier<0>();
+        // The next tile's first stage and scales have landed, and the last stage's slot is free.
+        if (stages % kPeriod == 0)
+            stage_barrier<kYounger>();
+        else  // its scales may be what was asked for last
+            stage_barrier<0>();
 
         // Lane l holds entries 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32 of a
         // 32 x 32 tile. Turned through LDS (each wavefront in its own part), they go
@@ -501,15 +514,18 @@ __global__ __launch_bounds__(64 * WV * WN, 2) void mxfp4_product_kernel(
                 __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             }
         }
-        if (!more)
+        if (!more) {
+            if constexpr (RING > 2)  // no load into LDS is out when the workgroup ends
+                stage_barrier<0>();
             return;
+        }
         cur = next;
-        slot ^= 1;
+        slot = in_ring(slot + 1);
         lds_barrier();  // all outputs have left LDS
     }
 }
 
-template <int TV, int TN, int WV, int WN, int PER_CU>
+template <int TV, int TN, int WV, int WN, int RING, int PER_CU>
 hipError_t launch_tile(int rows, int depth, int cols, const uint8_t* a, const uint8_t* a_scale,
                        const uint8_t* w, const uint8_t* w_scale, int out_dtype, void* out, hipStream_t s) {
     const long tiles_v = (static_cast<long>(cols) + TV - 1) / TV;
@@ -519,11 +535,11 @@ hipError_t launch_tile(int rows, int depth, int cols, const uint8_t* a, const ui
     // Workgroups stay for several tiles: as many as the chip holds at a time.
     const dim3 grid(static_cast<unsigned>(std::min(tiles_v * tiles_n, 256L * PER_CU))), block(64 * WV * WN);
     if (out_dtype == SPEC_BF16)
-        mxfp4_product_kernel<TV, TN, WV, WN, kBF16><<<grid, block, 0, s>>>(
+        mxfp4_product_kernel<TV, TN, WV, WN, RING, kBF16><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     else
-        mxfp4_product_kernel<TV, TN, WV, WN, kF32><<<grid, block, 0, s>>>(
+        mxfp4_product_kernel<TV, TN, WV, WN, RING, kF32><<<grid, block, 0, s>>>(
             a, a_scale, w, w_scale, rows, depth, cols, static_cast<int>(tiles_n),
             static_cast<int>(tiles_v * tiles_n), out);
     return hipGetLastError();
@@ -601,14 +617,20 @@ int spec_mxfp4_product(int rows, int depth, int cols, const uint8_t* a, const ui
     // 157 (100, 20011, depth 1024) 7.8 : 9.4, and with 64 rows and 152064 entries 83 : 82.
     // 64 against 32 with 33 rows and 32000 entries 21.5 : 23.0, with 64 and 152064 83 : 93;
     // 32 against 64 with 32 rows 20.8 : 21.6, and with 152064 entries 69.8 : 74.7.
+    // The small ones at depths that are worth it have four or five slots and half as many
+    // workgroups on a compute unit: 64 rows of 20000, 32000, 152064 entries 14.7 : 18.6,
+    // 18.8 : 22.0, 79.1 : 83.5, at a depth of 1024 32000 entries 7.5 : 7.4; 1 row of 32000
+    // 14.8 : 19.2, of 152064 59.6 : 62.5, 8 rows of 32000 at depths of 3200, 2304, 2048
+    // 14.1 : 17.2, 9.6 : 10.2, 9.1 : 9.0. (Of 128, on one workgroup, 128 x 152064 92 : 91.)
+    const bool deep = depth > 2048;
     if (rows > 128 && tiles(256, 256) >= 144)
-        SPEC_TILE(256, 256, 2, 4, 1);
+        SPEC_TILE(256, 256, 2, 4, 2, 1);
     else if (rows > 64 && tiles(128, 128) >= 224)
-        SPEC_TILE(128, 128, 2, 2, 2);
+        SPEC_TILE(128, 128, 2, 2, 2, 2);
     else if (rows > 32)
-        SPEC_TILE(64, 64, 1, 2, 4);
+        deep ? SPEC_TILE(64, 64, 1, 2, 4, 2) : SPEC_TILE(64, 64, 1, 2, 2, 4);
     else
-        SPEC_TILE(64, 32, 2, 1, 5);
+        deep ? SPEC_TILE(64, 32, 2, 1, 5, 2) : SPEC_TILE(64, 32, 2, 1, 2, 5);
 #undef SPEC_TILE
     return e == hipSuccess ? SPEC_OK : e == hipErrorInvalidValue ? SPEC_EINVAL : SPEC_EHIP;
 }

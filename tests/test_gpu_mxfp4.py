@@ -157,7 +157,8 @@ def test_product(N, D, V, dtype):
     # several tiles for a workgroup of every tile, of one stage, two, three and five
     (3, 128, 90001), (20, 384, 85000), (32, 640, 82000), (5, 1152, 82003), (40, 128, 70001), (64, 384, 66000),
     (33, 640, 65700), (60, 1152, 65601), (70, 128, 70001), (128, 384, 66003), (100, 640, 66000), (66, 1152, 65700),
-    (512, 128, 33000), (300, 384, 36001), (257, 640, 33003), (512, 1152, 32900),
+    (3, 2176, 40001), (20, 2432, 33300), (32, 2688, 33003), (5, 4096, 34000), (40, 2176, 33001), (64, 2432, 33300),
+    (33, 2688, 33003), (60, 4096, 34000), (512, 128, 33000), (300, 384, 36001), (257, 640, 33003), (512, 1152, 32900),
 ])
 def test_product_in_the_larger_tiles(N, D, V, dtype):
     print(f"\n[mxfp4 N={N} D={D} V={V} {dtype}]", flush=True)
