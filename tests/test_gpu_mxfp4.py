@@ -136,9 +136,11 @@ def check_product(a, sa, w, sw, dtype, out):
 SHAPES = [(1, 128, 1), (1, 256, 8), (3, 128, 5), (1, 512, 4096), (16, 1024, 1000), (17, 384, 129), (33, 256, 127),
           (64, 512, 2056), (65, 4096, 300), (128, 128, 128), (130, 640, 513), (200, 2048, 1111), (256, 512, 4099),
           (300, 4096, 520), (513, 128, 260), (1000, 896, 777),
-          # few rows: wavefronts that share a tile's depth, rows that LDS holds and does not, more tiles than wavefronts
+          # few rows: small tiles, at depths with two slots and with more
           (1, 4096, 300), (40, 4096, 999), (64, 4096, 1000), (33, 8192, 500), (7, 2176, 130), (32, 16384, 70),
-          (64, 1024, 70001), (5, 256, 130001), (32, 4224, 9001)]
+          (64, 1024, 70001), (5, 256, 130001), (32, 4224, 9001),
+          # the largest depth
+          (2, 1 << 20, 33), (70, 1 << 20, 130)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
