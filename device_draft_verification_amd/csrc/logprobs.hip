@@ -160,14 +160,17 @@ struct Selection {
         }
     }
 
-    // A first bar: every wavefront has its share of keep threads whose largest entry
-    // reaches it.
-    __device__ void begin(float most) {
+    // A first bar: each of the first `waves` wavefronts, whose threads all have entries,
+    // has its share of keep threads whose largest one reaches it.
+    __device__ void begin(float most, int waves) {
+        waves = min(waves, T / 64);
+        if (waves == 0)
+            return;
         const uint32_t v[1] = {ordered32(most + 0.0f)};
         const uint32_t least = over_lanes(v[0], [](uint32_t a, uint32_t b) { return min(a, b); });
-        const uint32_t mine = kth_largest<1, LOW>(v, 1, (keep + T / 64 - 1) / (T / 64),
+        const uint32_t mine = kth_largest<1, LOW>(v, 1, (keep + waves - 1) / waves,
                                                   __builtin_amdgcn_readfirstlane(least));
-        lds.bars[threadIdx.x >> 6] = mine;
+        lds.bars[threadIdx.x >> 6] = static_cast<int>(threadIdx.x >> 6) < waves ? mine : ~0u;
         lds_barrier();
         uint32_t b = lds.bars[0];
 #pragma unroll
@@ -611,7 +614,7 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
                     if (put_aside > kAside)
                         select_lds.lost = 1;
                     if (first) {
-                        sel.begin(most);
+                        sel.begin(most, (g1 - g0) / 64);
                         bar_z = logit_at_least(static_cast<uint32_t>(sel.bar >> 32));
                         narrow_aside();
                     }
@@ -688,7 +691,7 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
 #pragma unroll
                     for (int i = 0; i < W; ++i)
                         before += static_cast<int>(__popcll(__ballot(!(z[i] <= above))));
-                    if (at == token_group) {  // ties in front of the token in its own group
+                    if (at == token_group && at < g1) {  // ties in front of the token in its own group
                         const int to = static_cast<int>(token - r.element(at));
 #pragma unroll
                         for (int i = 0; i < W; ++i)
@@ -782,7 +785,7 @@ __global__ __launch_bounds__(kT) void logprobs_merge_kernel(LogprobsArgs a, int 
         for (int i = 1; i < kHeld; ++i)
             best = own[i] > best ? own[i] : best;
         if (total > kCap / 4)
-            sel.begin(best ? key_logit(best) : kNegMax);
+            sel.begin(best ? key_logit(best) : kNegMax, total / 64);
         sel.close(true, [&]() {
             bool has[kHeld];
 #pragma unroll
@@ -909,7 +912,10 @@ Split split_of(int rows, int vocab, int dtype) {
     const long steps = (groups + kStep - 1) / kStep;
     const long want = std::max(1, kAtOnce / rows);
     const long per = (steps + want - 1) / want;
-    return {static_cast<int>((steps + per - 1) / per), static_cast<int>(per * kStep)};
+    // Of the same length, in whole lines: a short one at the end has no bar to begin with
+    // (1 x 50000 bf16, a list of 20: @A@ us for @B@).
+    const long splits = (steps + per - 1) / per;
+    return {static_cast<int>(splits), static_cast<int>(((groups + splits - 1) / splits + 7) / 8 * 8)};
 }
 
 }  // namespace

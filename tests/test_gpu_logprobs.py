@@ -166,6 +166,17 @@ def test_orders_that_crowd_the_lists(kind, N, dtype):
     check(z[sub], token[sub], None, K, {k: v[at] for k, v in got.items()})
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_masked_tokens_at_the_ends_of_rows(dtype):
+    """Their rank counts what is masked in front of them too, once."""
+    for V in (9001, 9003, 9006, 20005):
+        z = torch.randn(40, V, generator=torch.Generator().manual_seed(V)).to(DTYPE[dtype])
+        token = torch.cat((torch.arange(20), torch.arange(V - 20, V))).int().cuda()
+        z[:, :25] = z[:, V - 25:] = -float("inf")
+        z = z.cuda()
+        check(z, token, None, 4, scores(z, token, None, 4))
+
+
 def test_lists_longer_than_what_is_there():
     z = torch.full((3, 20000), -float("inf"))
     z[0, 5000:5003] = torch.tensor([1.0, 3.0, 2.0])
