@@ -463,7 +463,7 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
 // ten instructions with the unpacking, the largest entry and the token's rank. Bound by
 // those and by the read at nearly the same rate: 2304 x 152064 bf16 take 121 us without
 // a list, 5.8 TB/s, and 149 us with lists of 64, 4.7 TB/s (a plain read: 7.1). Few rows
-// are bound by latency: 1 x 128256 fp32 with a list of 20 takes 8.7 us and 4.8 to join
+// are bound by latency: 1 x 128256 fp32 with a list of 20 takes 9 us and 4.8 to join
 // its 32 parts. Steps of 256 threads x 4 groups: of 512 or 128 threads, of 2 or 6 groups
 // measured slower; five workgroups on a compute unit instead of four 160 us for 176.
 template <int DT, int T, int U, bool TOP>
@@ -830,8 +830,8 @@ struct BackwardArgs {
 // With l = log p = (x - M) - log S: grad = p (c0 + c1 l), c0 = -r (a + b H) and
 // c1 = -r b, and r a more at the token. Bound by reading and writing the row. One
 // step of a workgroup's loads per split: workgroups follow the rows, so that
-// together they read and write one advancing front: 2304 x 152064 bf16 take 228 us,
-// 6.1 TB/s, the rate of a large copy.
+// together they read and write one advancing front: 2304 x 152064 bf16 take 226 us,
+// 6.2 TB/s, the rate of a large copy.
 constexpr int kBackU = 5;
 
 template <int DT>
