@@ -622,10 +622,12 @@ __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int spli
                 auto end = [&](bool first, bool last) {
                     if (put_aside > kAside)
                         select_lds.lost = 1;
+                    wave_order();  // groups are read by other lanes than put them aside
                     if (first) {
                         sel.begin(most, (g1 - g0) / 64);
                         bar_z = logit_at_least(static_cast<uint32_t>(sel.bar >> 32));
                         narrow_aside();
+                        wave_order();
                     }
                     const bool done = sel.close(last, [&]() {
                         // Lane by lane the next entry that reaches the bar: most groups have one.

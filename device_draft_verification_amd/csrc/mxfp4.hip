@@ -487,9 +487,7 @@ __global__ __launch_bounds__(64 * WV * WN, RING > 2 ? 1 : 2) void mxfp4_product_
                         else
                             *reinterpret_cast<float4*>(to) = make_float4(z[0], z[1], z[2], z[3]);
                     }
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                wave_order();
                 constexpr int kEntries = 32 * kTurnV;
                 const int vb = cur.v0 + wv + 32 * i0;
                 if (whole) {
@@ -509,9 +507,7 @@ __global__ __launch_bounds__(64 * WV * WN, RING > 2 ? 1 : 2) void mxfp4_product_
                             static_cast<elem_t*>(out)[static_cast<size_t>(nb + r) * cols + vb + lane] =
                                 *reinterpret_cast<const elem_t*>(turn + r * kRowBytes + lane * ESZ);
                 }
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                wave_order();
             }
         }
         if (!more) {

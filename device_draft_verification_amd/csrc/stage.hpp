@@ -22,6 +22,15 @@ __device__ __forceinline__ void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// What a wavefront's lanes wrote to LDS before it is there for all its lanes behind it. The
+// LDS keeps a wavefront's accesses in order, so that this is no instruction; without it
+// the compiler may take them for one lane's own.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The workgroup's barrier for exchanges through LDS: unlike __syncthreads it
 // does not wait for global loads, so that a row stays on its way while its list
 // is reduced. The empty asm keeps the compiler from moving accesses across.
