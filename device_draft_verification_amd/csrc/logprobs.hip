@@ -105,13 +105,16 @@ __device__ inline uint32_t kth_largest(const uint32_t (&v)[N], int n, int k, uin
 // the order in which keys arrive.
 constexpr int kCap = 512;  // keys
 
+// Wavefronts meet at barriers only: what one reads here behind a barrier is written
+// again behind another one. counts and lost, which a segment's end reads and the next
+// segment's writes, have that barrier where close() ends (1 to 5 a row).
 template <int T>
 struct SelectionLds {
     alignas(16) uint64_t lists[2][kCap];
-    uint64_t bar;
+    uint64_t bar;      // of rank(), read by close() behind a barrier and by nobody else
     int counts[2];     // keys put into the lists, also those that one had no place for
     int lost;          // groups that a wavefront had no place for
-    uint32_t bars[T / 64];  // the wavefronts' first ones
+    uint32_t bars[T / 64];  // the wavefronts' first ones, written once
 };
 
 template <int T, int G>
@@ -222,8 +225,11 @@ struct Selection {
         // Before the last ranking more keys are cheaper than a narrower list.
         if (n > (last ? 3 * keep : keep + 16))
             narrow();
-        if (!last && held > keep + 64)  // that many are equal
+        if (last)  // what follows begins with sort(), which writes the other list
+            return true;
+        if (held > keep + 64)  // that many are equal
             sort();
+        lds_barrier();  // all have read counts and lost, which the next segment writes
         return true;
     }
 

@@ -4,6 +4,8 @@ does a lane between two exchanges. Rows must come out the same in every order, w
 that waits where others do not."""
 import ctypes
 import glob
+import itertools
+import multiprocessing
 import os
 import subprocess
 
@@ -26,6 +28,8 @@ REPLACED = {
          "r = a != a ? a : b != b ? b : fmaxf(a, b);")],
 }
 HOST_PART = "bool aligned(const void* p, size_t a)"     # from here on the source is the host's
+
+fork = multiprocessing.get_context("fork")
 
 pytestmark = pytest.mark.skipif(not os.path.exists(CLANG), reason="needs clang's vector types")
 
@@ -77,9 +81,23 @@ def scores(lib, z, token, keep, order, splits=1, dtype="bf16"):
     out = dict(logprob=f(N), rank=i(N), entropy=f(N), top_token=i(N, keep), top_logprob=f(N, keep), norm=f(N, 2))
     P = ctypes.c_void_p
     token, order = np.ascontiguousarray(token, np.int32), np.asarray(order, np.int32)
-    fault = lib.run_scores(1 if dtype == "bf16" else 0, int(keep > 0), N, V, keep, splits, per, P(order.ctypes.data),
-                           P(raw.ctypes.data + at), P(token.ctypes.data), None,
-                           *[P(x.ctypes.data) for x in out.values()])
+
+    def call(to):
+        fault = lib.run_scores(1 if dtype == "bf16" else 0, int(keep > 0), N, V, keep, splits, per, P(order.ctypes.data),
+                               P(raw.ctypes.data + at), P(token.ctypes.data), None,
+                               *[P(x.ctypes.data) for x in out.values()])
+        to.send((fault, out))
+
+    # in a process of its own: wavefronts that disagree may leave their arrays
+    here, there = fork.Pipe(duplex=False)
+    child = fork.Process(target=call, args=(there,))
+    child.start()
+    there.close()
+    try:
+        fault, out = here.recv()
+    except EOFError:
+        fault = b"the process ended"
+    child.join()
     return fault, out, values
 
 
@@ -120,3 +138,35 @@ def test_rows_of_one_segment(lib, V, dtype, order):
         fault, got, values = scores(lib, z, [V // 3], keep, order, dtype=dtype)
         assert fault is None, (fault, V, keep, order)
         check(got, values, [V // 3], keep)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("kind", ["normal", "rising", "levels", "late", "uneven"])
+def test_rows_of_several_segments(lib, kind, order):
+    V = 41003                                            # segments of 1, 3 and 2 steps
+    for keep, seed in ((20, 1), (64, 2), (1, 3)):
+        z = rows(kind, V, seed)
+        token = [int(np.argmax(z))] if seed == 1 else [V // 2]
+        fault, got, values = scores(lib, z, token, keep, order)
+        assert fault is None, (fault, kind, keep, order)
+        check(got, values, token, keep)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+def test_rows_in_parts(lib, order):
+    V = 41003
+    z, token = rows("normal", V, 5), [17]
+    for splits, keep, dtype in ((2, 20, "f32"), (5, 64, "bf16")):
+        fault, got, values = scores(lib, z, token, keep, order, splits, dtype)
+        assert fault is None, (fault, splits, order)
+        check(got, values, token, keep)
+
+
+def test_any_order_gives_the_same_list(lib):
+    """Entries that many segments keep, every order of the four wavefronts."""
+    V = 26000
+    z = rows("normal", V, 9)
+    for order in itertools.permutations(range(4)):
+        fault, got, values = scores(lib, z, [3], 8, order)
+        assert fault is None, (fault, order)
+        check(got, values, [3], 8)
