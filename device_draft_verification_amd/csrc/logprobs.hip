@@ -842,6 +842,15 @@ struct BackwardArgs {
 // 6.2 TB/s, the rate of a large copy.
 constexpr int kBackU = 5;
 
+// The exponential instruction gives 0 for results below 2^-126 (a log p under
+// kSubnormal), whose products with large coefficients are ordinary numbers, and with
+// others subnormal ones. There it forms 2^120 p, and the coefficient is taken times
+// 2^-120: what it still loses, p below 2^-246, times a coefficient of at
+// most 1e25 * 201 is less than half of the smallest number. So p is 0 below kNothing
+// (at -inf the product with log p would be NaN).
+constexpr float kSubnormal = -87.0f, kNothing = -200.0f;
+constexpr float kRaise = 120.0f, kLower = 0x1p-120f;
+
 template <int DT>
 __global__ __launch_bounds__(kT) void logprobs_backward_kernel(BackwardArgs a, int splits, int per_split) {
     using Row = RowGroups<DT>;
@@ -870,9 +879,9 @@ __global__ __launch_bounds__(kT) void logprobs_backward_kernel(BackwardArgs a, i
     const double rb = a.grad_entropy ? scale * static_cast<double>(a.grad_entropy[row]) : 0.0;
     const double d0 = -(ra + (rb == 0.0 ? 0.0 : rb * static_cast<double>(a.entropy[row]))), d1 = -rb;
     const float c0 = static_cast<float>(d0), c1 = static_cast<float>(d1);
-    // Coefficients that binary32 holds with room for what they are multiplied by;
-    // the others (and NaNs) go by binary64.
-    const bool near = fabs(d0) <= 1e30 && fabs(d1) <= 1e30;
+    // Coefficients that binary32 holds with room for what they are multiplied by, and
+    // that leave nothing of a p below 2^-246; the others (and NaNs) go by binary64.
+    const bool near = fabs(d0) <= 1e25 && fabs(d1) <= 1e25;
     const long hot = token >= 0 ? r.group_of(token) : -1;
     for (int g = g0;;) {
 #pragma unroll
@@ -880,22 +889,38 @@ __global__ __launch_bounds__(kT) void logprobs_backward_kernel(BackwardArgs a, i
             const int at = g + tid + u * kT;
             if (at >= g1)
                 continue;
-            float z[W], d[W];
+            float z[W], l[W], d[W];
             Row::unpack(q[u], z);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                // below -200 p is 0 (and the product with l would be NaN at -inf)
-                const float l = fmaxf((scale_logit(z[i], inv_t) - m) - log_s, -200.0f);
-                d[i] = fast_exp2(l * kLog2e) * __builtin_fmaf(c1, l, c0);
+                l[i] = fmaxf((scale_logit(z[i], inv_t) - m) - log_s, kNothing);
+                d[i] = fast_exp2(l[i] * kLog2e) * __builtin_fmaf(c1, l[i], c0);
+            }
+            float least = l[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i)
+                least = fminf(least, l[i]);
+            if (least < kSubnormal) {
+                bool some = false;  // or masked entries alone
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    some |= l[i] < kSubnormal && l[i] > kNothing;
+                if (some) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        if (l[i] < kSubnormal)
+                            d[i] = fast_exp2(__builtin_fmaf(l[i], kLog2e, kRaise)) *
+                                   (__builtin_fmaf(c1, l[i], c0) * kLower);
+                }
             }
             if (at == hot || !near) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    const double l = fmax((static_cast<double>(scale_logit(z[i], inv_t)) - static_cast<double>(m)) -
-                                              static_cast<double>(log_s), -800.0);
+                    const double far = fmax((static_cast<double>(scale_logit(z[i], inv_t)) - static_cast<double>(m)) -
+                                                static_cast<double>(log_s), -800.0);
                     const bool one = r.element(at) + i == token;
                     if (one || !near)
-                        d[i] = static_cast<float>((one ? ra : 0.0) + exp(l) * (d0 + d1 * l));
+                        d[i] = static_cast<float>((one ? ra : 0.0) + exp(far) * (d0 + d1 * far));
                 }
             }
             store_group<DT>(r, out, at, whole, d);
