@@ -916,11 +916,11 @@ __global__ __launch_bounds__(kT) void logprobs_backward_kernel(BackwardArgs a, i
             if (at == hot || !near) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    const double far = fmax((static_cast<double>(scale_logit(z[i], inv_t)) - static_cast<double>(m)) -
-                                                static_cast<double>(log_s), -800.0);
+                    const float x = scale_logit(z[i], inv_t);
+                    const double far = fmax((static_cast<double>(x) - static_cast<double>(m)) - static_cast<double>(log_s), -800.0);
                     const bool one = r.element(at) + i == token;
-                    if (one || !near)
-                        d[i] = static_cast<float>((one ? ra : 0.0) + exp(far) * (d0 + d1 * far));
+                    if (one || !near)  // a masked entry has none, also of weights that are not finite
+                        d[i] = static_cast<float>((one ? ra : 0.0) + (x == -inf ? 0.0 : exp(far) * (d0 + d1 * far)));
                 }
             }
             store_group<DT>(r, out, at, whole, d);

@@ -256,7 +256,9 @@ def score_grad_scaled(x, token, a, b, r):
     """Gradient of sum_n (a logprob + b entropy) for z with x = r z: valid rows only."""
     l, p, h = score_parts(x)
     a = np.where(token >= 0, a, 0.0)
-    g = -p * (a[:, None] + b[:, None] * (np.where(p > 0, l, 0.0) + h[:, None]))
+    with np.errstate(invalid="ignore"):
+        g = -p * (a[:, None] + b[:, None] * (np.where(p > 0, l, 0.0) + h[:, None]))
+    g[np.isneginf(x)] = 0.0   # whatever the weights
     at = np.nonzero(token >= 0)[0]
     g[at, token[at]] += a[at]
     return g * r[:, None]

@@ -47,3 +47,22 @@ def test_a_masked_token_has_the_gradient_of_the_formula(V, dtype):
     want[torch.arange(N), token.long()] = 0.5 * 0.75
     want[7] = 0
     assert torch.equal(grad[masked], want[masked])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_masked_entries_of_rows_with_weights_that_are_not_finite(dtype):
+    """0 as ever, though nothing times such a weight is NaN; the row's other entries are not finite."""
+    inf, nan = float("inf"), float("nan")
+    N, V = 6, 9001
+    z = torch.randn(N, V, generator=torch.Generator().manual_seed(1))
+    z[:, 100:4000] = z[:, V - 3:] = -INF
+    z = z.to(DTYPE[dtype]).cuda()
+    masked = torch.isinf(z)
+    token = torch.tensor([5, 5, 5, 5, 200, -1], dtype=torch.int32, device="cuda")
+    a = torch.tensor([inf, nan, 1.0, -inf, nan, inf], device="cuda")
+    b = torch.tensor([0.0, 1.0, nan, inf, 0.0, 0.5], device="cuda")
+    grad = score_and_gradient(z, token, None, a, b)[2]
+    masked[4, 200] = False                            # the token itself: r a
+    assert torch.isnan(grad[4, 200])
+    assert (grad[masked] == 0).all()
+    assert not torch.isfinite(grad[:5][~masked[:5]]).any() and torch.isfinite(grad[5]).all()

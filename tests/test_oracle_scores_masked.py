@@ -18,3 +18,12 @@ def test_a_masked_token_has_the_gradient_of_the_formula():
     x = torch.tensor(z[:1] / 2).double().requires_grad_()
     torch.log_softmax(x, 1)[0, 1].backward()
     assert x.grad[0, 1] == 1 and x.grad[0, 3] == 0
+
+
+def test_masked_entries_have_no_gradient_whatever_the_weights():
+    z = np.array([[1.0, -np.inf, 0.5]] * 3, np.float32)
+    token = np.array([0, 0, -1], np.int32)
+    a, b = np.array([np.inf, 1, np.nan], np.float32), np.array([0, np.nan, 1], np.float32)
+    with np.errstate(invalid="ignore"):
+        g = ops.token_scores_grad(z, token, None, a, b)
+    assert (g[:, 1] == 0).all() and not np.isfinite(g[:2, [0, 2]]).any() and np.isfinite(g[2]).all()
