@@ -275,6 +275,10 @@ __global__ __launch_bounds__(64 * WV * WN, RING > 2 ? 1 : 2) void mxfp4_product_
     static_assert(TV % (8 * kWavesHere) == 0 && TN % (8 * kWavesHere) == 0,
                   "every wavefront issues the same loads");
     static_assert(kWavesHere % 2 == 0, "a lane's chunk is the same in all loads");
+    // Loads find a row of a tile by a 24-bit multiplication, in 32 bits.
+    constexpr long kMostBytes = SPEC_MXFP4_MAX_DEPTH / 2;
+    static_assert(kMostBytes < 1L << 24 && (TV > TN ? TV : TN) * kMostBytes <= 1L << 32,
+                  "a tile's offsets stay inside the multiplication and its word");
     // The epilogue turns 32 rows of up to 128 bytes of a wavefront's outputs through LDS
     // at a time, in the slot of the last stage.
     constexpr int ESZ = OUT == kBF16 ? 2 : 4;

@@ -63,7 +63,8 @@ extern "C" {
 /* Entries that a row of D entries is padded to. */
 #define SPEC_MXFP4_PADDED(D) (((D) + 127) / 128 * 128)
 
-/* Largest depth of the product (the bound above; a row of codes stays below 2^31 bits). */
+/* Largest depth of the product: the sum's bound above is 2^-9 of sum_k |A W| there. (The
+ * kernel's addresses would hold to a depth below 2^25.) */
 #define SPEC_MXFP4_MAX_DEPTH (1 << 20)
 
 int spec_mxfp4_quantize_rows(int rows, int cols, int dtype, const void* x, uint8_t* out_q,
