@@ -468,9 +468,9 @@ __device__ inline void write_row(const LogprobsArgs& a, long row, const Part& p,
 // distance, its exponential, and one multiply-add and one addition to the sums, about
 // ten instructions with the unpacking, the largest entry and the token's rank. Bound by
 // those and by the read at nearly the same rate: 2304 x 152064 bf16 take 121 us without
-// a list, 5.8 TB/s, and 149 us with lists of 64, 4.7 TB/s (a plain read: 7.1). Few rows
-// are bound by latency: 1 x 128256 fp32 with a list of 20 takes 9 us and 4.8 to join
-// its 32 parts. Steps of 256 threads x 4 groups: of 512 or 128 threads, of 2 or 6 groups
+// a list, 5.8 TB/s, and 152 us with lists of 64, 4.6 TB/s (a plain read: 7.1); 1152 x
+// 152064 fp32 118 and 132 us. Few rows are bound by latency: 1 x 128256 fp32 with a list
+// of 20 takes 9 us and 4.8 to join its 32 parts. Steps of 256 threads x 4 groups: of 512 or 128 threads, of 2 or 6 groups
 // measured slower; five workgroups on a compute unit instead of four 160 us for 176.
 template <int DT, int T, int U, bool TOP>
 __global__ __launch_bounds__(T, 5) void logprobs_kernel(LogprobsArgs a, int splits, int per_split,
@@ -838,8 +838,8 @@ struct BackwardArgs {
 // With l = log p = (x - M) - log S: grad = p (c0 + c1 l), c0 = -r (a + b H) and
 // c1 = -r b, and r a more at the token. Bound by reading and writing the row. One
 // step of a workgroup's loads per split: workgroups follow the rows, so that
-// together they read and write one advancing front: 2304 x 152064 bf16 take 226 us,
-// 6.2 TB/s, the rate of a large copy.
+// together they read and write one advancing front: 2304 x 152064 bf16 take 223 to 228
+// us, 1152 x 152064 fp32 220 to 228, 6.1 to 6.4 TB/s, the rate of a large copy.
 constexpr int kBackU = 5;
 
 // The exponential instruction gives 0 for results below 2^-126 (a log p under
@@ -943,7 +943,10 @@ constexpr int kAtOnce = 256 * 5;
 // Parts of a row when there are `rows`: as many as are at work at once, none shorter
 // than a step. Measured against half as many and half as many more (us, bf16, lists of
 // 20): 64 rows of 152064 21.4 : 24.2 and 21.2, 256 rows 35.2 : 37.3 and 42.5, 900 rows of
-// 32000, which stay whole, 26.0 : 26.0 and 35.3.
+// 32000, which stay whole, 26.0 : 26.0 and 35.3. Rows that leave places empty, or fill
+// them a second time in part, are not better off in more parts (of 152064; one part
+// first): 600 rows, the last that are split, 59.8 : 55.5 in two; 650 59.1 : 65.0, 800
+// 67.0 : 72.2, 1290 98.7 : 100.6, 1500 101.6 : 110.1.
 struct Split {
     int splits, per_split;
 };

@@ -148,8 +148,9 @@ struct Eight {
 
 // The exponent comes from the largest magnitude's bits; the conversion instructions
 // scale, round to nearest even and saturate. Bound by memory: 152064 x 4096 bf16 with
-// their values in place take 454 us, 6.2 TB/s, the rate of a large copy; 2304 x 4001
-// fp32, whose rows start anywhere, 13.5 us.
+// their values in place take 454 us, 6.2 TB/s, the rate of a large copy, without values
+// 256; 2304 x 4001 fp32, whose rows start anywhere, 13.5 us with values, 76032 x 4096
+// fp32 252 without.
 //
 // A lane takes eight entries, four lanes a block, 16 blocks a wavefront, over all
 // rows as one sequence (a padded row is a whole number of lanes' entries, 16 or
@@ -225,8 +226,8 @@ __global__ __launch_bounds__(kBlock) void mxfp4_quantize_kernel(const void* x, i
 // With many rows a stage of 256 x 256 is a chain of its loads, a barrier, reads of 192
 // KB from LDS (a quarter of the cycles) and the matrix instructions (45 % of them):
 // 2304 x 152064 outputs at depth 4096 take 780-815 us, 3.6 PFLOP/s, where a loop of
-// nothing but these instructions reaches 6.2 to 6.8 on such data (the clock falls under
-// their power) and the kernel without its loads took 557. Few rows are bound by the read of the weights
+// nothing but these instructions reaches 6.1 to 6.8 on such data (the clock falls under
+// their power) and the kernel without its loads took 557 to 570. Few rows are bound by the read of the weights
 // and its latency: 64 x 152064 at depth 4096 take 79 us, 4.4 TB/s, 1 x 152064 60 us,
 // 5.5 TB/s, 1 x 32000 14 us, 5 TB/s. Slower: stages of half the length and four
 // slots 860 us (then 810), 4 wavefronts of 128 x 128 each, alone on their SIMDs, 885.
@@ -622,6 +623,10 @@ int spec_mxfp4_product(int rows, int depth, int cols, const uint8_t* a, const ui
     // 18.8 : 22.0, 79.1 : 83.5, at a depth of 1024 32000 entries 7.5 : 7.4; 1 row of 32000
     // 14.8 : 19.2, of 152064 59.6 : 62.5, 8 rows of 32000 at depths of 3200, 2304, 2048
     // 14.1 : 17.2, 9.6 : 10.2, 9.1 : 9.0. (Of 128, on one workgroup, 128 x 152064 92 : 91.)
+    // The rule counts tiles, not the rounds that workgroups go through them, nor rows that
+    // a tile leaves empty; with 152064 entries (its side, then the next ones): 96 rows 128
+    // 87, 256 110, 64 111; 160 rows 256 116, 128 122; 192 119 : 127; 256 126 : 138; 400
+    // 187 : 216; 512 197 : 240; 1024 377 : 463; but 300 rows 177 : 170.
     const bool deep = depth > 2048;
     if (rows > 128 && tiles(256, 256) >= 144)
         SPEC_TILE(256, 256, 2, 4, 2, 1);

@@ -37,10 +37,10 @@
  *   out_grad[n][v] = r (a ([v = t] - p_v) - b p_v (log p_v + H)),
  * the derivative of sum_n (a logprob + b entropy) with respect to z[n][v]; p
  * and H from norm and entropy, which the forward call returned. a counts as 0
- * in rows without a token. Gradients are 0 at masked entries, but for the token
- * itself where that is masked (r a, as p_t = 0; its logprob is -inf), 0 in rows
- * with nothing but masked entries, NaN throughout in a row whose scores are NaN
- * (a token >= V included), and rounded once to the logits' dtype.
+ * in rows without a token. Gradients are 0 at masked entries, whatever a and b,
+ * but for the token itself where that is masked (r a, as p_t = 0; its logprob is
+ * -inf), 0 in rows with nothing but masked entries, NaN throughout in a row whose
+ * scores are NaN (a token >= V included), and rounded once to the logits' dtype.
  *
  * Layouts: dense row-major DEVICE arrays owned by the caller: logits, out_grad
  * [N, V] in the context's dtype (aligned to the element, any V), token, out_rank

@@ -8,7 +8,8 @@ Pinned in tests/test_oracle_draft_ops.py: the selection by sorting Python tuples
 torch's log_softmax in float64, the gradient by autograd and by central differences, the
 quantisation by exact fractions, the product by Python integers; the 4-bit forms and the scores in
 tests/test_oracle_scores.py, by a table's nearest entry, exact fractions, Python sorting, torch's
-log_softmax and autograd in float64, and central differences.
+log_softmax and autograd in float64, and central differences; the gradient at masked entries in
+tests/test_oracle_scores_masked.py.
 """
 from __future__ import annotations
 
